@@ -4,8 +4,8 @@
  * A C ABI over hand-written HIP kernels. Plain pointers and sizes only; the
  * library allocates nothing, keeps no state between calls and is safe to call
  * from several host threads at once. Every call is asynchronous on the
- * caller's HIP stream: it validates its arguments on the host, enqueues one
- * kernel and returns. Faults during execution surface at the caller's next
+ * caller's HIP stream: it validates its arguments on the host, enqueues its
+ * kernel (the sort of a long list and the clipping: two or more) and returns. Faults during execution surface at the caller's next
  * synchronisation, not here.
  *
  * What the quantize computes (the pages "MX Microscaling: Quantize,
@@ -74,8 +74,18 @@ enum mxq_status {
     MXQ_E_HIP = 8,       /* the HIP runtime refused the launch                */
     MXQ_E_FLAGS = 9,     /* unknown bits in a flags argument                  */
     MXQ_E_RES_DTYPE = 10, /* dequantize result type is not F32 or BF16        */
-    MXQ_E_DIM = 11        /* quantize axis is not -1 / -2 (or 1 / 0)          */
+    MXQ_E_DIM = 11,       /* quantize axis is not -1 / -2 (or 1 / 0)          */
+    MXQ_E_MOE = 12,       /* experts, slots per token or group alignment out  */
+                          /* of range, or a negative token count              */
+    MXQ_E_ROWS = 13,      /* negative or unaligned count of sorted rows, or a */
+                          /* negative count of tensors or elements            */
+    MXQ_E_ELEM_DTYPE = 14, /* element type is not BF16, F16 or F32 (ids: not  */
+                          /* 4 or 8 bytes)                                    */
+    MXQ_E_VALUE = 15      /* max_norm is negative or NaN                      */
 };
+
+/* Element types of the calls that take plain tensors. */
+enum mxq_elem_dtype { MXQ_ELEM_BF16 = 0, MXQ_ELEM_F16 = 1, MXQ_ELEM_F32 = 2 };
 
 /* Result types of mxq_dequantize. */
 enum mxq_res_dtype { MXQ_RES_F32 = 0, MXQ_RES_BF16 = 1 };
@@ -291,6 +301,178 @@ int mxq_scaled_matmul(const void *lhs, const void *lhs_scale, const void *rhs, c
 int mxq_scaled_matmul_quantize(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs_scale,
                                int64_t P, int64_t M, int64_t N, int fmt, int out_dtype, unsigned flags,
                                void *data_out, void *scale_out, void *stream);
+
+/*
+ * Mixture of experts
+ * ==================
+ *
+ * Token t (of `tokens`) is sent to up to `slots` experts; pair t * slots + j is
+ * its j-th choice. The sorted rows hold the pairs expert by expert, in pair
+ * order within an expert; each expert's group of rows starts at a multiple of
+ * `align` (32, the rows of an MX block, wherever a product's contraction runs
+ * over sorted rows). How many rows a batch needs is known only on the device,
+ * so buffers hold mxq_moe_rows() rows, enough for any assignment, and the
+ * calls agree on what the rows without a pair hold: zeros.
+ *
+ *   offsets  int32 [experts + 1]: group e is rows offsets[e] .. offsets[e + 1]
+ *            - 1 (its pairs first, then rows without one)
+ *   src      int32 [rows]: the pair of a row, -1 without one
+ *   dest     int32 [tokens, slots]: the row of a pair, -1 without one
+ *
+ * The calls read these from device memory and check each use: an entry out
+ * of range is a row without a pair (or a pair without a row), never an access
+ * out of bounds.
+ */
+#define MXQ_MOE_MAX_EXPERTS 1024
+#define MXQ_MOE_MAX_SLOTS 64
+#define MXQ_MOE_MAX_ALIGN 256
+
+/* Sorted rows that hold any assignment of tokens * slots pairs to `experts`
+ * experts: at most min(experts, pairs) groups, each with up to align - 1 rows
+ * without a pair. -1 for invalid arguments. */
+int64_t mxq_moe_rows(int64_t tokens, int64_t slots, int64_t experts, int64_t align);
+
+/* Workspace of mxq_moe_sort (0: none needed, or invalid arguments). */
+size_t mxq_moe_sort_workspace_bytes(int64_t tokens, int64_t slots, int64_t experts);
+
+/*
+ * mxq_moe_sort -- pairs sorted by expert.
+ *
+ *   ids        device pointer, [tokens, slots] expert numbers, int32 or int64;
+ *              a number outside 0 .. experts - 1 is a pair without a row (an
+ *              expert on another device, a dropped token).
+ *   id_bytes   4 or 8, else MXQ_E_ELEM_DTYPE.
+ *   experts    1 .. MXQ_MOE_MAX_EXPERTS; slots 1 .. MXQ_MOE_MAX_SLOTS.
+ *   align      multiple of 4, 4 .. MXQ_MOE_MAX_ALIGN.
+ *   offsets, src, dest   as above, every entry written (src:
+ *              mxq_moe_rows(tokens, slots, experts, align) of them).
+ *   workspace  mxq_moe_sort_workspace_bytes() bytes; may be NULL for 0.
+ * All pointers 16-byte aligned. The order does not depend on the launch:
+ * equal inputs give equal outputs.
+ */
+int mxq_moe_sort(const void *ids, int id_bytes, int64_t tokens, int64_t slots, int64_t experts, int64_t align,
+                 int32_t *offsets, int32_t *src, int32_t *dest, void *workspace, void *stream);
+
+/*
+ * mxq_moe_gather_quantize -- token rows gathered into sorted order and
+ * MX-quantized in the same pass.
+ *
+ * The bytes are those of mxq_quantize_axis on the [rows, K] tensor whose row r
+ * is x[src[r] / slots], or zeros where src[r] is no pair: with dim -1 the
+ * operand of a product with the experts' weights (mxq_grouped_matmul), with
+ * dim -2 that of their gradient (mxq_grouped_matmul_wgrad).
+ *
+ *   x          device pointer, [tokens, K] BF16/F16, row-major.
+ *   dim        -1 (K a multiple of 32) or -2 (rows a multiple of 32), or 1, 0.
+ *   flags      MXQ_FLAG_*; the grouped products read dense scales.
+ *   src, rows  from mxq_moe_sort; rows a multiple of 4. With rows > 0, at
+ *              least one token.
+ *   data_out   mxq_data_bytes(K / 4, 4 * rows, out_dtype) bytes for dim -1,
+ *              mxq_data_bytes(rows / 4, 4 * K, out_dtype) for dim -2.
+ *   scale_out  mxq_scale_bytes() of the same P and F.
+ * All pointers 16-byte aligned.
+ */
+int mxq_moe_gather_quantize(const void *x, int64_t tokens, int64_t slots, int64_t K, int in_dtype, int out_dtype,
+                            int dim, unsigned flags, const int32_t *src, int64_t rows, void *data_out,
+                            void *scale_out, void *stream);
+
+/*
+ * mxq_moe_combine -- results brought back to token order:
+ *     out[t] = sum over j of weights[t][j] * y[dest[t][j]],
+ * added in slot order in fp32 and rounded once. A pair without a row adds
+ * nothing; a token without any gives zeros. weights NULL: all 1, which is
+ * also the gradient of the gather.
+ *
+ *   y, out     device pointers, [rows, N] and [tokens, N] of elem_dtype.
+ *   N          any length >= 0.
+ *   weights    fp32 [tokens, slots], or NULL.
+ * All pointers 16-byte aligned.
+ */
+int mxq_moe_combine(const void *y, int64_t rows, int64_t N, int elem_dtype, const int32_t *dest,
+                    const float *weights, int64_t tokens, int64_t slots, void *out, void *stream);
+
+/*
+ * mxq_moe_combine_backward -- the gradient of mxq_moe_combine:
+ *     grad_y[r]          = weights[src[r]] * grad[src[r] / slots], zeros for a
+ *                          row without a pair
+ *     grad_weights[t][j] = sum over n of grad[t][n] * y[dest[t][j]][n] (fp32),
+ *                          0 for a pair without a row
+ * grad [tokens, N], y and grad_y [rows, N] of elem_dtype; src and dest of one
+ * mxq_moe_sort. All pointers 16-byte aligned; every element written.
+ */
+int mxq_moe_combine_backward(const void *grad, const void *y, int64_t rows, int64_t N, int elem_dtype,
+                             const int32_t *src, const int32_t *dest, const float *weights, int64_t tokens,
+                             int64_t slots, void *grad_y, float *grad_weights, void *stream);
+
+/*
+ * mxq_grouped_matmul -- the experts' products:
+ *     out[r][n] = sum over k < 4P of L[k][r] * R_g[k][n] for r in group g,
+ * zeros for the rows past the last group. Operand layout, element values and
+ * accumulation as for mxq_scaled_matmul, with dense scales.
+ *
+ *   lhs, lhs_scale  P x 4*rows FP8 data and [P/8, rows] scales: the sorted
+ *                   rows, quantized along K (mxq_moe_gather_quantize or
+ *                   mxq_quantize_axis with dim -1, dense).
+ *   rhs, rhs_scale  [groups, P, 4N] data and [groups, P/8, N] scales: the
+ *                   weights [K, N] of each expert, quantized with dim -2; or,
+ *                   for the gradient of the input, the weights [N', K'] with
+ *                   dim -1 (P = K'/4, N = N').
+ *   offsets         int32 [groups + 1] on the device; entries multiples of 4.
+ *   groups          1 .. MXQ_MOE_MAX_EXPERTS.
+ *   P               multiple of 8 (0: a zero result); rows and N multiples of
+ *                   4, up to MXQ_MATMUL_MAX_COLS.
+ *   out             [rows, N] of res_dtype (enum mxq_res_dtype).
+ * All pointers 16-byte aligned.
+ */
+int mxq_grouped_matmul(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs_scale,
+                       const int32_t *offsets, int64_t groups, int64_t P, int64_t rows, int64_t N, int fmt,
+                       int res_dtype, void *out, void *stream);
+
+/*
+ * mxq_grouped_matmul_wgrad -- the gradient of the experts' weights:
+ *     out[g][m][n] = sum over the sorted rows r of group g of L[r][m] * R[r][n],
+ * zeros for an empty group.
+ *
+ *   lhs, lhs_scale  P x 4M FP8 data and [P/8, M] scales: the sorted rows
+ *                   (4P of them) of the forward input, quantized with dim -2.
+ *   rhs, rhs_scale  P x 4N data and [P/8, N] scales: the gradient of the
+ *                   result, the same way.
+ *   offsets         as above, entries multiples of 32.
+ *   out             [groups, M, N] of res_dtype.
+ * All pointers 16-byte aligned; M and N multiples of 4.
+ */
+int mxq_grouped_matmul_wgrad(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs_scale,
+                             const int32_t *offsets, int64_t groups, int64_t P, int64_t M, int64_t N, int fmt,
+                             int res_dtype, void *out, void *stream);
+
+/* Workspace of mxq_clip_grad_norm; 0 for invalid arguments. The three arrays
+ * are host memory. */
+size_t mxq_clip_grad_norm_workspace_bytes(const int64_t *elements, const int *elem_dtypes, int64_t count);
+
+/*
+ * mxq_clip_grad_norm -- many tensors scaled by their global norm:
+ *     norm   = sqrt(sum of the squares of all elements of all tensors)
+ *     factor = max_norm / norm where max_norm < norm < infinity, else 1
+ *     out    = round(g * factor)
+ * The squares are added in 64 bits; the factor and the norm that is returned
+ * are rounded to fp32 (a norm beyond its range is returned as infinity; the
+ * factor is still that of the 64-bit norm). An infinity or NaN among the
+ * elements leaves the values as they are; the norm tells.
+ *
+ *   grads, outs  host arrays of `count` device pointers, each aligned to its
+ *                element; outs NULL: the norm only. outs[i] == grads[i] scales
+ *                in place; otherwise they do not overlap.
+ *   elements     host array, elements per tensor (0 allowed), each tensor
+ *                contiguous.
+ *   elem_dtypes  host array of enum mxq_elem_dtype.
+ *   max_norm     >= 0 (MXQ_E_VALUE; not read without outs).
+ *   norm         device pointer, one fp32.
+ *   workspace    mxq_clip_grad_norm_workspace_bytes() bytes, 16-byte aligned.
+ * The host arrays are read before the call returns. Equal inputs give equal
+ * outputs: nothing depends on the order of the workgroups.
+ */
+int mxq_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *elements, const int *elem_dtypes,
+                       int64_t count, double max_norm, float *norm, void *workspace, void *stream);
 
 /* Human-readable message for a status code (static storage, never NULL;
  * "unknown status" for a code not listed above). The messages restate the

@@ -13,12 +13,15 @@ import ctypes
 import functools
 import os
 import threading
+from typing import NamedTuple
 
 import torch  # loaded first so that the library binds to torch's HIP runtime
 
 __all__ = [
-    "IN_DTYPES", "OUT_DTYPES", "RES_DTYPES", "MXQError", "quantize", "dequantize", "quantize_axis", "scaled_matmul",
-    "scaled_matmul_quantize", "data_bytes", "scale_image_bytes", "result_bytes", "data_shape", "scale_image_shape",
+    "IN_DTYPES", "OUT_DTYPES", "RES_DTYPES", "ELEM_DTYPES", "MXQError", "quantize", "dequantize", "quantize_axis",
+    "scaled_matmul", "scaled_matmul_quantize", "MoEPlan", "moe_rows", "moe_sort", "moe_gather_quantize", "moe_combine",
+    "moe_combine_backward", "grouped_scaled_matmul", "grouped_scaled_matmul_wgrad", "clip_grad_norm", "grad_norm",
+    "data_bytes", "scale_image_bytes", "result_bytes", "data_shape", "scale_image_shape",
     "axis_view_shape", "logical_scale_view", "status_string", "library_path", "load",
 ]
 
@@ -28,6 +31,7 @@ _LIB_NAME = "libmxq.so"
 IN_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 OUT_DTYPES = {"e4m3fn": 0, "e5m2": 1, "e2m1": 2}
 RES_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+ELEM_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 FLAG_ALT_EMAX = 1
 FLAG_DENSE_SCALE = 2
 ABI_VERSION = 1
@@ -91,6 +95,27 @@ def load():
         lib.mxq_dequantize.restype = c.c_int
         lib.mxq_result_bytes.argtypes = [c.c_int64, c.c_int64, c.c_int]
         lib.mxq_result_bytes.restype = c.c_size_t
+        p, i64 = c.c_void_p, c.c_int64
+        lib.mxq_moe_rows.argtypes = [i64, i64, i64, i64]
+        lib.mxq_moe_rows.restype = i64
+        lib.mxq_moe_sort_workspace_bytes.argtypes = [i64, i64, i64]
+        lib.mxq_moe_sort_workspace_bytes.restype = c.c_size_t
+        lib.mxq_moe_sort.argtypes = [p, c.c_int, i64, i64, i64, i64, p, p, p, p, p]
+        lib.mxq_moe_sort.restype = c.c_int
+        lib.mxq_moe_gather_quantize.argtypes = [p, i64, i64, i64, c.c_int, c.c_int, c.c_int, c.c_uint, p, i64, p, p, p]
+        lib.mxq_moe_gather_quantize.restype = c.c_int
+        lib.mxq_moe_combine.argtypes = [p, i64, i64, c.c_int, p, p, i64, i64, p, p]
+        lib.mxq_moe_combine.restype = c.c_int
+        lib.mxq_moe_combine_backward.argtypes = [p, p, i64, i64, c.c_int, p, p, p, i64, i64, p, p, p]
+        lib.mxq_moe_combine_backward.restype = c.c_int
+        for name in ("mxq_grouped_matmul", "mxq_grouped_matmul_wgrad"):
+            fn = getattr(lib, name)
+            fn.argtypes = [p, p, p, p, p, i64, i64, i64, i64, c.c_int, c.c_int, p, p]
+            fn.restype = c.c_int
+        lib.mxq_clip_grad_norm_workspace_bytes.argtypes = [p, p, i64]
+        lib.mxq_clip_grad_norm_workspace_bytes.restype = c.c_size_t
+        lib.mxq_clip_grad_norm.argtypes = [p, p, p, p, i64, c.c_double, p, p, p]
+        lib.mxq_clip_grad_norm.restype = c.c_int
         lib.mxq_status_string.argtypes = [c.c_int]
         lib.mxq_status_string.restype = c.c_char_p
         lib.mxq_abi_version.argtypes = []
@@ -385,3 +410,310 @@ def quantize_axis(x: torch.Tensor, out_dtype: str = "e4m3fn", dim: int = -1, dat
     _check(_call_on(x.device, lib.mxq_quantize_axis, x.data_ptr(), R, C, IN_DTYPES[x.dtype], code, dim, flags,
                     data_out.data_ptr(), scale_out.data_ptr(), sh))
     return data_out, scale_out
+
+
+# ---------------------------------------------------------------------------
+# Mixture of experts
+# ---------------------------------------------------------------------------
+
+class MoEPlan(NamedTuple):
+    """Where each (token, slot) pair goes when a batch is sorted by expert
+    (int32 device tensors, see :func:`moe_sort`)."""
+
+    offsets: torch.Tensor   # [experts + 1]: group e is sorted rows offsets[e] .. offsets[e + 1] - 1
+    src: torch.Tensor       # [rows]: the pair t * slots + j of a sorted row, -1 without one
+    dest: torch.Tensor      # [tokens, slots]: the sorted row of a pair, -1 without one
+
+
+def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """An output or workspace for a kernel on ``stream``: allocated on that
+    stream, so that neither its memory's earlier use nor its next one can
+    overlap the kernel."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _check_tensor(name: str, t: torch.Tensor, shape, dtypes, device: torch.device | None = None) -> None:
+    """A contiguous device tensor of this shape (None: any extent) and one of
+    these types, on ``device`` if given."""
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError("%s must be a device tensor%s" % (name, "" if device is None else " on %s" % device))
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError("%s must have shape %s, got %s"
+                         % (name, "[%s]" % ", ".join("*" if n is None else str(n) for n in shape), tuple(t.shape)))
+    if t.dtype not in dtypes:
+        raise ValueError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+_INT32 = (torch.int32,)
+_FLOAT32 = (torch.float32,)
+_UINT8 = (torch.uint8,)
+
+
+def _elem_code(dtype: torch.dtype) -> int:
+    try:
+        return ELEM_DTYPES[dtype]
+    except KeyError:
+        raise MXQError(14, "element type must be bfloat16, float16 or float32, got %s" % dtype) from None
+
+
+def moe_rows(tokens: int, slots: int, experts: int, align: int = 32) -> int:
+    """Sorted rows that hold any assignment of ``tokens * slots`` pairs to
+    ``experts`` experts with groups aligned to ``align`` rows."""
+    rows = int(load().mxq_moe_rows(tokens, slots, experts, align))
+    if rows < 0:
+        raise MXQError(12, "tokens %d, slots %d, experts %d, align %d" % (tokens, slots, experts, align))
+    return rows
+
+
+def moe_sort(experts: torch.Tensor, num_experts: int, align: int = 32,
+             stream: torch.cuda.Stream | None = None) -> MoEPlan:
+    """Sort the (token, slot) pairs of a batch by expert.
+
+    ``experts`` [tokens, slots] int32 or int64 holds each pair's expert; a
+    number outside 0 .. ``num_experts`` - 1 is a pair without a row here.
+    Pairs keep their order within an expert, and every expert's group of rows
+    starts at a multiple of ``align`` (a multiple of 4 up to 256; 32 where the
+    weight gradients are to be computed). Nothing is copied to the host: the
+    plan has :func:`moe_rows` rows, whatever the assignment.
+    """
+    lib = load()
+    _check_tensor("experts", experts, (None, None), (torch.int32, torch.int64))
+    T, k = experts.shape
+    dev = experts.device
+    rows = moe_rows(T, k, num_experts, align)
+    nws = int(lib.mxq_moe_sort_workspace_bytes(T, k, num_experts))
+    offsets = _new((num_experts + 1,), torch.int32, dev, stream)
+    src = _new((rows,), torch.int32, dev, stream)
+    dest = _new((T, k), torch.int32, dev, stream)
+    ws = _new((nws,), torch.uint8, dev, stream) if nws else None
+    _check(_call_on(dev, lib.mxq_moe_sort, experts.data_ptr(), experts.element_size(), T, k, num_experts, align,
+                    offsets.data_ptr(), src.data_ptr(), dest.data_ptr(), ws.data_ptr() if nws else None,
+                    _stream_handle(stream, dev)))
+    return MoEPlan(offsets, src, dest)
+
+
+def _check_plan(plan: MoEPlan, device: torch.device):
+    """(rows, tokens, slots) of a plan on ``device``."""
+    _check_tensor("plan.src", plan.src, (None,), _INT32, device)
+    _check_tensor("plan.dest", plan.dest, (None, None), _INT32, device)
+    return (plan.src.shape[0],) + tuple(plan.dest.shape)
+
+
+def moe_gather_quantize(x: torch.Tensor, plan: MoEPlan, out_dtype: str = "e4m3fn", dim: int = -1,
+                        data_out: torch.Tensor | None = None, scale_out: torch.Tensor | None = None,
+                        stream: torch.cuda.Stream | None = None, alt_emax: bool = False, dense_scale: bool = True):
+    """Gather the rows of ``x`` [tokens, K] (bf16/f16) into sorted order and
+    quantize them.
+
+    Returns the ``(data, scale)`` that :func:`quantize_axis` with ``dim`` gives
+    for the [rows, K] tensor whose row r is the row of ``x`` that
+    ``plan.src[r]`` names, or zeros: with ``dim=-1`` the left operand of
+    :func:`grouped_scaled_matmul`, with ``dim=-2`` an operand of
+    :func:`grouped_scaled_matmul_wgrad`. Scales are dense by default, as the
+    grouped products read them.
+    """
+    lib = load()
+    code = _out_code(out_dtype)
+    if x.dtype not in IN_DTYPES:
+        raise MXQError(1, "input must be bfloat16 or float16, got %s" % x.dtype)
+    _check_tensor("x", x, (None, None), tuple(IN_DTYPES))
+    rows, T, k = _check_plan(plan, x.device)
+    K = x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError("x has %d rows, the plan %d tokens" % (x.shape[0], T))
+    P, F = axis_view_shape(rows, K, dim)
+    flags = (FLAG_ALT_EMAX if alt_emax else 0) | (FLAG_DENSE_SCALE if dense_scale else 0)
+    if data_out is None:
+        data_out = _new(data_shape(P, F, out_dtype), torch.uint8, x.device, stream)
+    if scale_out is None:
+        scale_out = _new(scale_image_shape(P, F, dense_scale), torch.uint8, x.device, stream)
+    _check_out_buffer("data_out", data_out, _data_nbytes(P, F, code), x.device)
+    _check_out_buffer("scale_out", scale_out, _scale_nbytes(P, F, flags), x.device)
+    _check(_call_on(x.device, lib.mxq_moe_gather_quantize, x.data_ptr(), T, k, K, IN_DTYPES[x.dtype], code, dim, flags,
+                    plan.src.data_ptr(), rows, data_out.data_ptr(), scale_out.data_ptr(),
+                    _stream_handle(stream, x.device)))
+    return data_out, scale_out
+
+
+def moe_combine(y: torch.Tensor, plan: MoEPlan, weights: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """Bring sorted rows back to token order: out[t] = sum over j of
+    weights[t, j] * y[dest[t, j]], added in float32 in slot order.
+
+    ``y`` [rows, N] is bf16, f16 or f32, ``weights`` [tokens, slots] float32
+    (None: all 1, the gradient of the gather). A pair without a row adds
+    nothing. Returns [tokens, N] of y's type.
+    """
+    lib = load()
+    code = _elem_code(y.dtype)
+    _check_tensor("y", y, (None, None), tuple(ELEM_DTYPES))
+    rows, T, k = _check_plan(plan, y.device)
+    if y.shape[0] != rows:
+        raise ValueError("y has %d rows, the plan %d" % (y.shape[0], rows))
+    N = y.shape[1]
+    if weights is not None:
+        _check_tensor("weights", weights, (T, k), _FLOAT32, y.device)
+    if out is None:
+        out = _new((T, N), y.dtype, y.device, stream)
+    else:
+        _check_tensor("out", out, (T, N), (y.dtype,), y.device)
+    _check(_call_on(y.device, lib.mxq_moe_combine, y.data_ptr(), rows, N, code, plan.dest.data_ptr(),
+                    None if weights is None else weights.data_ptr(), T, k, out.data_ptr(),
+                    _stream_handle(stream, y.device)))
+    return out
+
+
+def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, plan: MoEPlan, weights: torch.Tensor,
+                         grad_y: torch.Tensor | None = None, grad_weights: torch.Tensor | None = None,
+                         stream: torch.cuda.Stream | None = None):
+    """The gradients ``(grad_y, grad_weights)`` of :func:`moe_combine` with
+    weights, given the gradient ``grad`` [tokens, N] of its result.
+
+    grad_y [rows, N] (y's type) is zero in the rows without a pair,
+    grad_weights [tokens, slots] (float32) for the pairs without a row. (The
+    gradient of the unweighted combine is the gather.)
+    """
+    lib = load()
+    code = _elem_code(y.dtype)
+    _check_tensor("y", y, (None, None), tuple(ELEM_DTYPES))
+    rows, T, k = _check_plan(plan, y.device)
+    if y.shape[0] != rows:
+        raise ValueError("y has %d rows, the plan %d" % (y.shape[0], rows))
+    N = y.shape[1]
+    _check_tensor("grad", grad, (T, N), (y.dtype,), y.device)
+    _check_tensor("weights", weights, (T, k), _FLOAT32, y.device)
+    if grad_y is None:
+        grad_y = _new((rows, N), y.dtype, y.device, stream)
+    else:
+        _check_tensor("grad_y", grad_y, (rows, N), (y.dtype,), y.device)
+    if grad_weights is None:
+        grad_weights = _new((T, k), torch.float32, y.device, stream)
+    else:
+        _check_tensor("grad_weights", grad_weights, (T, k), _FLOAT32, y.device)
+    _check(_call_on(y.device, lib.mxq_moe_combine_backward, grad.data_ptr(), y.data_ptr(), rows, N, code,
+                    plan.src.data_ptr(), plan.dest.data_ptr(), weights.data_ptr(), T, k, grad_y.data_ptr(),
+                    grad_weights.data_ptr(), _stream_handle(stream, y.device)))
+    return grad_y, grad_weights
+
+
+def grouped_scaled_matmul(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs: torch.Tensor, rhs_scale: torch.Tensor,
+                          offsets: torch.Tensor, fmt: str = "e4m3fn", res_dtype: torch.dtype = torch.bfloat16,
+                          out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The experts' products: out[r] = X[r] @ W_g for the sorted rows r of
+    group g, zeros for the rows past the last group.
+
+    ``lhs`` [P, 4 rows] with dense scales [P/8, rows] are the sorted rows
+    quantized along K = 4P (:func:`moe_gather_quantize`, or
+    :func:`quantize_axis` with ``dim=-1, dense_scale=True``); ``rhs``
+    [groups, P, 4N] with [groups, P/8, N] the experts' weights [K, N], each
+    quantized with ``dim=-2`` (for the gradient of the input: the weights with
+    ``dim=-1``); ``offsets`` [groups + 1] from :func:`moe_sort`. Returns
+    [rows, N] float32 or bfloat16. Groups and arithmetic as in
+    :func:`scaled_matmul`.
+    """
+    lib = load()
+    code = _out_code(fmt)
+    if res_dtype not in RES_DTYPES:
+        raise MXQError(10, "result type must be float32 or bfloat16, got %s" % res_dtype)
+    _check_tensor("lhs", lhs, (None, None), _UINT8)
+    dev = lhs.device
+    P, M = lhs.shape[0], lhs.shape[1] // 4
+    _check_tensor("rhs", rhs, (None, P, None), _UINT8, dev)
+    G, N = rhs.shape[0], rhs.shape[2] // 4
+    if lhs.shape[1] % 4 or rhs.shape[2] % 4 or P % 8:
+        raise ValueError("lhs [P, 4 rows] and rhs [groups, P, 4 N] need P % 8 == 0")
+    _check_tensor("lhs_scale", lhs_scale, (P // 8, M), _UINT8, dev)
+    _check_tensor("rhs_scale", rhs_scale, (G, P // 8, N), _UINT8, dev)
+    _check_tensor("offsets", offsets, (G + 1,), _INT32, dev)
+    if out is None:
+        out = _new((M, N), res_dtype, dev, stream)
+    else:
+        _check_tensor("out", out, (M, N), (res_dtype,), dev)
+    _check(_call_on(dev, lib.mxq_grouped_matmul, lhs.data_ptr(), lhs_scale.data_ptr(), rhs.data_ptr(),
+                    rhs_scale.data_ptr(), offsets.data_ptr(), G, P, M, N, code, RES_DTYPES[res_dtype], out.data_ptr(),
+                    _stream_handle(stream, dev)))
+    return out
+
+
+def grouped_scaled_matmul_wgrad(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs: torch.Tensor,
+                                rhs_scale: torch.Tensor, offsets: torch.Tensor, fmt: str = "e4m3fn",
+                                res_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                                stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The gradient of the experts' weights: out[g] = X_g^T @ dY_g over the
+    sorted rows of group g, zeros for an empty group.
+
+    ``lhs`` [P, 4M] and ``rhs`` [P, 4N] with dense scales [P/8, M] and
+    [P/8, N] are the 4P sorted rows of the forward input [rows, M] and of the
+    result's gradient [rows, N], quantized with ``dim=-2``; the groups in
+    ``offsets`` [groups + 1] start at multiples of 32. Returns [groups, M, N].
+    """
+    lib = load()
+    code = _out_code(fmt)
+    if res_dtype not in RES_DTYPES:
+        raise MXQError(10, "result type must be float32 or bfloat16, got %s" % res_dtype)
+    P, M, N = _check_operands(lhs, lhs_scale, rhs, rhs_scale, True)
+    dev = lhs.device
+    _check_tensor("offsets", offsets, (None,), _INT32, dev)
+    G = offsets.shape[0] - 1
+    if out is None:
+        out = _new((max(G, 0), M, N), res_dtype, dev, stream)
+    else:
+        _check_tensor("out", out, (G, M, N), (res_dtype,), dev)
+    _check(_call_on(dev, lib.mxq_grouped_matmul_wgrad, lhs.data_ptr(), lhs_scale.data_ptr(), rhs.data_ptr(),
+                    rhs_scale.data_ptr(), offsets.data_ptr(), G, P, M, N, code, RES_DTYPES[res_dtype], out.data_ptr(),
+                    _stream_handle(stream, dev)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Gradient norm and clipping
+# ---------------------------------------------------------------------------
+
+def _norm_call(grads, max_norm, outs, stream):
+    lib = load()
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no tensors")
+    dev = grads[0].device
+    for name, ts in (("grads", grads), ("out", outs or ())):
+        for t in ts:
+            _check_tensor(name, t, (None,) * t.dim(), tuple(ELEM_DTYPES), dev)
+    if outs is not None and (len(outs) != len(grads) or
+                             any(o.dtype != g.dtype or o.shape != g.shape for o, g in zip(outs, grads))):
+        raise ValueError("out must hold a tensor of each gradient's shape and type")
+    n = len(grads)
+    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    optrs = None if outs is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
+    numels = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    codes = (ctypes.c_int * n)(*[ELEM_DTYPES[g.dtype] for g in grads])
+    norm = _new((), torch.float32, dev, stream)
+    ws = _new((int(lib.mxq_clip_grad_norm_workspace_bytes(numels, codes, n)),), torch.uint8, dev, stream)
+    _check(_call_on(dev, lib.mxq_clip_grad_norm, ptrs, optrs, numels, codes, n, max_norm, norm.data_ptr(),
+                    ws.data_ptr(), _stream_handle(stream, dev)))
+    return norm
+
+
+def grad_norm(grads, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The norm of all elements of all tensors (bf16, f16 or f32, mixed), as a
+    float32 device scalar; the squares are added in 64 bits."""
+    return _norm_call(grads, 0.0, None, stream)
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """Scale contiguous device tensors by max_norm / norm where their global
+    norm is finite and above ``max_norm``; return the norm (before scaling, a
+    float32 device scalar).
+
+    The tensors (bf16, f16 or f32, mixed) are scaled in place, or into the
+    tensors of ``out``. A norm that is not finite leaves the values as they
+    are. Nothing is copied to the host.
+    """
+    if not max_norm >= 0.0:
+        raise MXQError(15, "max_norm must not be negative or NaN, got %r" % (max_norm,))
+    grads = list(grads)
+    return _norm_call(grads, float(max_norm), grads if out is None else list(out), stream)

@@ -28,6 +28,10 @@ const char *mxq_status_string(int status)
     case MXQ_E_FLAGS: return "unknown flag bits";
     case MXQ_E_RES_DTYPE: return "dequantize result type must be F32 or BF16";
     case MXQ_E_DIM: return "quantize axis must be the last (-1) or second-to-last (-2) dimension";
+    case MXQ_E_MOE: return "experts, slots per token, tokens or the group alignment out of range";
+    case MXQ_E_ROWS: return "sorted rows must be a non-negative multiple of 4, and counts non-negative";
+    case MXQ_E_ELEM_DTYPE: return "element type must be BF16, F16 or F32 (expert numbers: int32 or int64)";
+    case MXQ_E_VALUE: return "max_norm must not be negative or NaN";
     default: return "unknown status";
     }
 }

@@ -1,0 +1,117 @@
+// mxq_grouped_api.hip -- mxq_grouped_matmul and mxq_grouped_matmul_wgrad:
+// validation, the choice of tile and the launch of the kernels in
+// mxq_grouped_kernels.hpp on the caller's stream.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mxq.h"
+#include "mxq_host.hpp"
+#include "mxq_grouped_kernels.hpp"
+
+namespace {
+
+using mxq_host::grid_fits;
+
+typedef void (*grouped_fn)(const uint8_t *, const uint8_t *, const uint8_t *, const uint8_t *, const int32_t *,
+                           uint32_t, uint32_t, uint32_t, uint32_t, uint32_t, void *);
+
+template <int FMT, int EPI> grouped_fn pick_kernel(int kind)
+{
+    switch (kind) {
+    case 0: return mxq::grouped_matmul_kernel<FMT, EPI, mxq::kGroupRows>;
+    case 1: return mxq::grouped_matmul_kernel<FMT, EPI, mxq::kGroupWgrad>;
+    case 2: return mxq::grouped_stream_kernel<FMT, EPI, 1, 4>;
+    default: return mxq::grouped_stream_kernel<FMT, EPI, 2, 4>;
+    }
+}
+
+grouped_fn pick(int fmt, int res_dtype, int kind)
+{
+    if (fmt == MXQ_OUT_E4M3FN)
+        return res_dtype == MXQ_RES_F32 ? pick_kernel<mxq::kOutE4M3FN, mxq::kEpiF32>(kind)
+                                        : pick_kernel<mxq::kOutE4M3FN, mxq::kEpiBF16>(kind);
+    return res_dtype == MXQ_RES_F32 ? pick_kernel<mxq::kOutE5M2, mxq::kEpiF32>(kind)
+                                    : pick_kernel<mxq::kOutE5M2, mxq::kEpiBF16>(kind);
+}
+
+// P % 8, column counts, types and pointers of both products; `empty`: no
+// operand byte is read.
+int check(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs_scale, const int32_t *offsets,
+          int64_t groups, int64_t P, int64_t M, int64_t N, int fmt, int res_dtype, const void *out, bool empty)
+{
+    if (fmt != MXQ_OUT_E4M3FN && fmt != MXQ_OUT_E5M2)
+        return MXQ_E_OUT_DTYPE;
+    if (res_dtype != MXQ_RES_F32 && res_dtype != MXQ_RES_BF16)
+        return MXQ_E_RES_DTYPE;
+    if (groups < 1 || groups > MXQ_MOE_MAX_EXPERTS)
+        return MXQ_E_MOE;
+    if (P < 0 || P % 8 != 0)
+        return MXQ_E_SHAPE_P8;
+    if (M < 0 || N < 0 || M % 4 != 0 || N % 4 != 0)
+        return MXQ_E_SHAPE_F4;
+    if (P > ((int64_t)1 << 29) - 1 || M > MXQ_MATMUL_MAX_COLS || N > MXQ_MATMUL_MAX_COLS)
+        return MXQ_E_OVERFLOW;
+    if (M == 0 || N == 0)
+        return MXQ_OK;
+    if (!offsets || !out || (!empty && (!lhs || !lhs_scale || !rhs || !rhs_scale)))
+        return MXQ_E_NULL;
+    if (((uintptr_t)lhs | (uintptr_t)lhs_scale | (uintptr_t)rhs | (uintptr_t)rhs_scale | (uintptr_t)out |
+         (uintptr_t)offsets) & 15u)
+        return MXQ_E_ALIGN;
+    return MXQ_OK;
+}
+
+int launch(grouped_fn k, int64_t blocks, uint32_t threads, const void *lhs, const void *lhs_scale, const void *rhs,
+           const void *rhs_scale, const int32_t *offsets, int64_t groups, int64_t P, int64_t M, int64_t N,
+           int64_t tiles_n, void *out, void *stream)
+{
+    const uint8_t *a0 = (const uint8_t *)lhs, *a1 = (const uint8_t *)lhs_scale, *a2 = (const uint8_t *)rhs,
+                  *a3 = (const uint8_t *)rhs_scale;
+    uint32_t g = (uint32_t)groups, p = (uint32_t)P, m = (uint32_t)M, n = (uint32_t)N, tn = (uint32_t)tiles_n;
+    void *args[] = {&a0, &a1, &a2, &a3, &offsets, &g, &p, &m, &n, &tn, &out};
+    const hipError_t err = hipLaunchKernel((const void *)k, dim3((uint32_t)blocks), dim3(threads), args, 0,
+                                           (hipStream_t)stream);
+    return err == hipSuccess ? MXQ_OK : MXQ_E_HIP;
+}
+
+} // namespace
+
+extern "C" {
+
+int mxq_grouped_matmul(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs_scale,
+                       const int32_t *offsets, int64_t groups, int64_t P, int64_t rows, int64_t N, int fmt,
+                       int res_dtype, void *out, void *stream)
+{
+    const int rc = check(lhs, lhs_scale, rhs, rhs_scale, offsets, groups, P, rows, N, fmt, res_dtype, out, P == 0);
+    if (rc != MXQ_OK || rows == 0 || N == 0)
+        return rc;
+    // Row tiles of any grouping of the rows: every group (and the rows past
+    // the last one) may end with a part of a tile. The tile follows from the
+    // mean rows per group.
+    const int64_t mean = rows / groups;
+    const int kind = mean <= 48 ? 2 : mean <= 96 ? 3 : 0;
+    const int64_t tile = kind == 2 ? 32 : kind == 3 ? 64 : mxq::kMmTile;
+    const int64_t cols = kind ? mxq::kStreamCols : mxq::kMmTile;
+    const uint32_t threads = kind ? 256 : mxq::kMmThreads;
+    const int64_t tiles_m = rows / tile + groups + 1, tiles_n = (N + cols - 1) / cols;
+    if (!grid_fits(tiles_m, tiles_n, threads))
+        return MXQ_E_OVERFLOW;
+    return launch(pick(fmt, res_dtype, kind), tiles_m * tiles_n, threads, lhs, lhs_scale, rhs, rhs_scale, offsets,
+                  groups, P, rows, N, tiles_n, out, stream);
+}
+
+int mxq_grouped_matmul_wgrad(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs_scale,
+                             const int32_t *offsets, int64_t groups, int64_t P, int64_t M, int64_t N, int fmt,
+                             int res_dtype, void *out, void *stream)
+{
+    const int rc = check(lhs, lhs_scale, rhs, rhs_scale, offsets, groups, P, M, N, fmt, res_dtype, out, P == 0);
+    if (rc != MXQ_OK || M == 0 || N == 0)
+        return rc;
+    const int64_t tiles_m = (M + mxq::kMmTile - 1) / mxq::kMmTile, tiles_n = (N + mxq::kMmTile - 1) / mxq::kMmTile;
+    if (!grid_fits(tiles_m, tiles_n, mxq::kMmThreads) || !grid_fits(tiles_m * tiles_n, groups, mxq::kMmThreads))
+        return MXQ_E_OVERFLOW;
+    return launch(pick(fmt, res_dtype, 1), tiles_m * tiles_n * groups, mxq::kMmThreads, lhs, lhs_scale, rhs,
+                  rhs_scale, offsets, groups, P, M, N, tiles_n, out, stream);
+}
+
+} // extern "C"

@@ -414,54 +414,28 @@ template <int F, int EPI>
 __device__ __attribute__((noinline)) void mm_rare_part(const uint8_t *lhs, const uint8_t *lhs_scale,
                                                        const uint8_t *rhs, const uint8_t *rhs_scale, uint32_t P,
                                                        uint32_t M, uint32_t N, uint32_t wm0, uint32_t wn0,
-                                                       uint32_t dense, void *out, uint8_t *out_scale, int emax_bias)
+                                                       uint32_t dense, void *out, uint8_t *out_scale, int emax_bias,
+                                                       uint32_t row_end)
 {
     const uint32_t lane = __lane_id();
     const uint32_t i = lane & 31u, h = lane >> 5;
     f32x16_t acc[2][4];
     mm_tile_255<F>(acc, lhs, lhs_scale, rhs, rhs_scale, P, M, N, wm0, wn0, dense, i, h);
-    mm_epilogue<EPI>(acc, wm0, wn0, M, N, out, out_scale, emax_bias, dense, i, h);
+    mm_epilogue<EPI>(acc, wm0, wn0, row_end, N, out, out_scale, emax_bias, dense, i, h);
 }
 
-// The kernel: one 256 x 256 result tile per workgroup, the main loop in
-// ping-pong, then the finiteness check, then the epilogue.
-template <int FMT, int EPI>
-__global__ __launch_bounds__(kMmThreads) void scaled_matmul_kernel(
-    const uint8_t *__restrict__ lhs, const uint8_t *__restrict__ lhs_scale, const uint8_t *__restrict__ rhs,
-    const uint8_t *__restrict__ rhs_scale, uint32_t P, uint32_t M, uint32_t N, uint32_t tiles_n, uint32_t dense,
-    void *__restrict__ out, uint8_t *__restrict__ out_scale, int emax_bias)
+// A workgroup's 256 x 256 tile of the product over operand rows 0 .. P - 1:
+// the main loop in ping-pong. Wave (grp, wq) ends with the sums of rows
+// 64 wq .., columns 128 grp .. of the tile in acc. `src` is the operand this
+// wave copies (lhs for grp = 0, rhs for grp = 1), from the tile's first
+// column on.
+template <int F>
+__device__ __forceinline__ void mm_tile_product(f32x16_t (&acc)[2][4], uint8_t *lds, const MmSource &src, uint32_t P,
+                                                uint32_t dense, uint32_t grp, uint32_t wq, uint32_t lane)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kMmStages * kMmStageBytes + kMmSpareBytes];
-    constexpr int F = MfmaFmt<FMT>::value;
-
-    const uint32_t tid = threadIdx.x;
-    const uint32_t lane = tid & 63u;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t grp = wave >> 2, wq = wave & 3u;
-    const uint32_t i = lane & 31u, h = lane >> 5;
-
-    // Tile order. Workgroup w runs on XCD w % 8, so XCD x is given the
-    // consecutive tile numbers [x * q, (x + 1) * q) (a tail stays in place).
-    // Tile numbers walk the output in groups of kMmGroupRows tile rows,
-    // column by column: the workgroups one XCD runs at a time cover a compact
-    // block (4 tile rows x 8 tile columns for 32 CUs) and share its operand
-    // panels in that XCD's L2.
-    const uint32_t ntiles = gridDim.x;
-    const uint32_t tiles_m = ntiles / tiles_n;
-    const uint32_t q = ntiles / kMmXcds;
-    const uint32_t w = blockIdx.x;
-    const uint32_t t = w < q * kMmXcds ? (w % kMmXcds) * q + w / kMmXcds : w;
-    const uint32_t group = t / (kMmGroupRows * tiles_n);
-    const uint32_t first_row = group * kMmGroupRows;
-    const uint32_t rows_in_group = min((uint32_t)kMmGroupRows, tiles_m - first_row);
-    const uint32_t in_group = t - group * kMmGroupRows * tiles_n;
-    const uint32_t m0 = (first_row + in_group % rows_in_group) * kMmTile;
-    const uint32_t n0 = (in_group / rows_in_group) * kMmTile;
-    const uint32_t wm = 64u * wq, wn = 128u * grp;
     const uint32_t nsteps = (P + kMmStepRows - 1) / kMmStepRows;
-
-    MmSource src;                                          // the operand this wave copies
-    mm_source(src, grp ? rhs : lhs, grp ? rhs_scale : lhs_scale, grp ? N : M, grp ? n0 : m0);
+    const uint32_t i = lane & 31u, h = lane >> 5;
+    const uint32_t wm = 64u * wq, wn = 128u * grp;
     const uint32_t t_off = grp ? kMmTileBytes : 0u;
     const bool has_scale = wq < 2u;
     const uint32_t s_off = 2u * kMmTileBytes + (grp ? kMmScaleBytes : 0u) + kMmTile * (wq & 1u);
@@ -473,7 +447,6 @@ __global__ __launch_bounds__(kMmThreads) void scaled_matmul_kernel(
     const uint32_t a_sc = 2u * kMmTileBytes + kMmTile * h + wm + 2u * i;
     const uint32_t b_sc = 2u * kMmTileBytes + kMmScaleBytes + kMmTile * h + wn + 4u * i;
 
-    f32x16_t acc[2][4];
 #pragma unroll
     for (int a = 0; a < 2; a++)
 #pragma unroll
@@ -543,6 +516,47 @@ __global__ __launch_bounds__(kMmThreads) void scaled_matmul_kernel(
     if (!grp)
         __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_s_waitcnt(kWaitAllCopies);
+}
+
+// The kernel: one 256 x 256 result tile per workgroup, the main loop in
+// ping-pong, then the finiteness check, then the epilogue.
+template <int FMT, int EPI>
+__global__ __launch_bounds__(kMmThreads) void scaled_matmul_kernel(
+    const uint8_t *__restrict__ lhs, const uint8_t *__restrict__ lhs_scale, const uint8_t *__restrict__ rhs,
+    const uint8_t *__restrict__ rhs_scale, uint32_t P, uint32_t M, uint32_t N, uint32_t tiles_n, uint32_t dense,
+    void *__restrict__ out, uint8_t *__restrict__ out_scale, int emax_bias)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kMmStages * kMmStageBytes + kMmSpareBytes];
+    constexpr int F = MfmaFmt<FMT>::value;
+
+    const uint32_t tid = threadIdx.x;
+    const uint32_t lane = tid & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t grp = wave >> 2, wq = wave & 3u;
+    const uint32_t i = lane & 31u, h = lane >> 5;
+
+    // Tile order. Workgroup w runs on XCD w % 8, so XCD x is given the
+    // consecutive tile numbers [x * q, (x + 1) * q) (a tail stays in place).
+    // Tile numbers walk the output in groups of kMmGroupRows tile rows,
+    // column by column: the workgroups one XCD runs at a time cover a compact
+    // block (4 tile rows x 8 tile columns for 32 CUs) and share its operand
+    // panels in that XCD's L2.
+    const uint32_t ntiles = gridDim.x;
+    const uint32_t tiles_m = ntiles / tiles_n;
+    const uint32_t q = ntiles / kMmXcds;
+    const uint32_t w = blockIdx.x;
+    const uint32_t t = w < q * kMmXcds ? (w % kMmXcds) * q + w / kMmXcds : w;
+    const uint32_t group = t / (kMmGroupRows * tiles_n);
+    const uint32_t first_row = group * kMmGroupRows;
+    const uint32_t rows_in_group = min((uint32_t)kMmGroupRows, tiles_m - first_row);
+    const uint32_t in_group = t - group * kMmGroupRows * tiles_n;
+    const uint32_t m0 = (first_row + in_group % rows_in_group) * kMmTile;
+    const uint32_t n0 = (in_group / rows_in_group) * kMmTile;
+    const uint32_t wm = 64u * wq, wn = 128u * grp;
+    MmSource src;                                          // the operand this wave copies
+    mm_source(src, grp ? rhs : lhs, grp ? rhs_scale : lhs_scale, grp ? N : M, grp ? n0 : m0);
+    f32x16_t acc[2][4];
+    mm_tile_product<F>(acc, lds, src, P, dense, grp, wq, lane);
 
     // The matrix cores read a scale byte of 255 as NaN, where it stands for
     // 2^128. A sum that is not finite may come from one, so the wave then
@@ -560,7 +574,7 @@ __global__ __launch_bounds__(kMmThreads) void scaled_matmul_kernel(
 
     if (__builtin_amdgcn_ballot_w64(!finite) != 0) {
         mm_rare_part<F, EPI>(lhs, lhs_scale, rhs, rhs_scale, P, M, N, m0 + wm, n0 + wn, dense, out, out_scale,
-                             emax_bias);
+                             emax_bias, M);
         // the wave ends here (no path back to the epilogue below, whose
         // sums would otherwise have to stay live across this branch)
         __builtin_amdgcn_endpgm();

@@ -1,0 +1,641 @@
+// mxq_moe_kernels.hpp -- gfx950 kernels around the experts of a
+// mixture-of-experts layer: pairs sorted by expert, token rows gathered into
+// that order and MX-quantized, results brought back to token order with their
+// weights, and that step's gradient.
+//
+// A pair is (token t, slot j), numbered t * slots + j. Sorted rows hold the
+// pairs expert by expert, in pair order within an expert, each expert's group
+// starting at a multiple of `align` rows:
+//   offsets[0] = 0, offsets[e + 1] = offsets[e] + align * ceil(count[e] / align)
+//   dest[pair] = the pair's row, -1 for a pair whose id is no expert's
+//   src[row]   = the row's pair, -1 for the rows between groups' ends and past
+//                the last group
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "mxq_axis_kernels.hpp"
+
+namespace mxq {
+
+// ----------------------------------------------------------------------------
+// Sort by expert
+// ----------------------------------------------------------------------------
+//
+// A counting sort. A workgroup of 16 waves takes a contiguous chunk of pairs,
+// a wave a contiguous part of the chunk. It counts its experts in LDS, one
+// row of counts per wave; the counts of everything before a wave's part then
+// give where its first pair of each expert goes, and each wave places its
+// pairs 64 at a time: lanes with the same expert find each other with one
+// ballot per bit of the expert number, their rank in that set gives the
+// order, and one of them advances the wave's position of that expert. Nothing
+// depends on the order in which waves or workgroups run.
+//
+// One workgroup sorts a short list in one launch. A longer one takes two
+// launches, of up to kSortBlocks workgroups: the counts of each chunk go to
+// the workspace, then every workgroup sums the chunks' counts itself (all of
+// them for the group sizes, those before its own for its positions).
+constexpr uint32_t kSortThreads = 1024;
+constexpr uint32_t kSortWaves = kSortThreads / 64;
+constexpr uint32_t kSortBlocks = 256;
+
+template <typename ID>
+__device__ __forceinline__ uint32_t sort_key(const ID *ids, uint32_t pair, uint32_t pairs, uint32_t experts)
+{
+    if (pair >= pairs)
+        return experts;
+    const ID id = ids[pair];
+    return id >= 0 && id < (ID)experts ? (uint32_t)id : experts;
+}
+
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t lane)
+{
+#pragma unroll
+    for (uint32_t d = 1; d < 64; d <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_up((int)v, d);
+        v += lane >= d ? o : 0u;
+    }
+    return v;
+}
+
+// Counts of this wave's part [first, last) of the pairs into row[0 .. experts).
+template <typename ID>
+__device__ __forceinline__ void sort_count(const ID *ids, uint32_t first, uint32_t last, uint32_t pairs,
+                                           uint32_t experts, uint32_t lane, uint32_t *row)
+{
+    for (uint32_t p = first; p < last; p += 64) {
+        const uint32_t key = sort_key(ids, p + lane, pairs, experts);
+        if (key < experts)
+            atomicAdd(row + key, 1u);
+    }
+}
+
+// Launch 1 of 2: counts[block][expert] of each workgroup's chunk. The 16 waves
+// share one row of LDS counts.
+template <typename ID>
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const ID *__restrict__ ids, uint32_t pairs,
+                                                                  uint32_t chunk, uint32_t experts,
+                                                                  uint32_t *__restrict__ counts)
+{
+    extern __shared__ uint32_t row[];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    for (uint32_t e = tid; e < experts; e += kSortThreads)
+        row[e] = 0;
+    __syncthreads();
+    const uint32_t part = chunk / kSortWaves;
+    const uint32_t first = blockIdx.x * chunk + wave * part;
+    sort_count(ids, first, first + part, pairs, experts, lane, row);
+    __syncthreads();
+    for (uint32_t e = tid; e < experts; e += kSortThreads)
+        counts[(uint64_t)blockIdx.x * experts + e] = row[e];
+}
+
+// Launch 2 of 2 (SINGLE = 0), or the whole sort in one workgroup (SINGLE = 1,
+// no counts in memory). Chunks are multiples of 64 * kSortWaves pairs and
+// blocks * chunk < 2^32 (checked on the host).
+//   LDS: kSortWaves rows of counts, then 3 arrays of experts: each group's
+//   pairs, the pairs of it before this chunk, its first row
+template <typename ID, int SINGLE>
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const ID *__restrict__ ids, uint32_t pairs,
+                                                                  uint32_t chunk, uint32_t experts, uint32_t align,
+                                                                  uint32_t rows, uint32_t key_bits,
+                                                                  const uint32_t *__restrict__ counts,
+                                                                  int32_t *__restrict__ offsets,
+                                                                  int32_t *__restrict__ src,
+                                                                  int32_t *__restrict__ dest)
+{
+    extern __shared__ uint32_t lds[];
+    __shared__ uint32_t wave_total[kSortWaves];
+    uint32_t *total = lds + kSortWaves * experts, *before = total + experts, *start = before + experts;
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    const uint32_t blocks = gridDim.x, block = blockIdx.x;
+
+    for (uint32_t n = tid; n < (kSortWaves + 2) * experts; n += kSortThreads)
+        lds[n] = 0;
+    __syncthreads();
+    const uint32_t part = chunk / kSortWaves;
+    const uint32_t first = block * chunk + wave * part;
+    uint32_t *mine = lds + wave * experts;
+    sort_count(ids, first, first + part, pairs, experts, lane, mine);
+    if constexpr (!SINGLE) {
+        // the workgroup's threads as rows of `width` experts: each row sums
+        // its share of the chunks
+        uint32_t width = 64;
+        while (width < experts)
+            width <<= 1;
+        const uint32_t e = tid & (width - 1), r = tid / width, n = kSortThreads / width;
+        uint32_t all = 0, prior = 0;
+        if (e < experts) {
+#pragma unroll 8
+            for (uint32_t b = r; b < blocks; b += n) {
+                const uint32_t c = counts[(uint64_t)b * experts + e];
+                all += c;
+                prior += b < block ? c : 0u;
+            }
+            atomicAdd(total + e, all);
+            atomicAdd(before + e, prior);
+        }
+    }
+    __syncthreads();
+
+    // thread e: group e's size, then the groups' first rows by a scan
+    const uint32_t e = tid;
+    uint32_t sum = 0;
+    if (e < experts) {
+        for (uint32_t w = 0; w < kSortWaves; w++) {
+            const uint32_t c = lds[w * experts + e];
+            lds[w * experts + e] = sum;   // pairs of this chunk before wave w
+            sum += c;
+        }
+        if constexpr (SINGLE)
+            total[e] = sum;
+        else
+            sum = total[e];
+    }
+    const uint32_t padded = (sum + align - 1) / align * align;
+    const uint32_t scan = wave_scan(padded, lane);
+    if (lane == 63)
+        wave_total[wave] = scan;
+    __syncthreads();
+    uint32_t base = 0;
+    for (uint32_t w = 0; w < wave; w++)
+        base += wave_total[w];
+    if (e < experts) {
+        const uint32_t at = base + scan - padded;
+        start[e] = at;
+        const uint32_t here = at + before[e];
+        for (uint32_t w = 0; w < kSortWaves; w++)
+            lds[w * experts + e] += here;
+        if (block == 0) {
+            offsets[e] = (int32_t)at;
+            if (e + 1 == experts)
+                offsets[experts] = (int32_t)(at + padded);
+        }
+    }
+    __syncthreads();
+
+    for (uint32_t p = first; p < first + part && p < pairs; p += 64) {
+        const uint32_t pair = p + lane;
+        const uint32_t key = sort_key(ids, pair, pairs, experts);
+        uint64_t same = __ballot(key < experts);
+        for (uint32_t b = 0; b < key_bits; b++) {
+            const uint64_t set = __ballot((key >> b) & 1u);
+            same &= (key >> b) & 1u ? set : ~set;
+        }
+        uint32_t row = 0;
+        const uint32_t leader = same ? (uint32_t)__builtin_ctzll(same) : lane;
+        if (key < experts && lane == leader)
+            row = atomicAdd(mine + key, (uint32_t)__popcll(same));
+        row = (uint32_t)__shfl((int)row, (int)leader) +
+              (uint32_t)__popcll(same & ((1ull << lane) - 1ull));
+        if (pair < pairs) {
+            dest[pair] = key < experts ? (int32_t)row : -1;
+            if (key < experts && row < rows)
+                src[row] = (int32_t)pair;
+        }
+    }
+    // rows without a pair: a wave per group, then past the last group
+    for (uint32_t g = block * kSortWaves + wave; g < experts; g += blocks * kSortWaves) {
+        const uint32_t end = g + 1 < experts ? start[g + 1] : start[g] + (total[g] + align - 1) / align * align;
+        for (uint32_t r = start[g] + total[g] + lane; r < end && r < rows; r += 64)
+            src[r] = -1;
+    }
+    const uint32_t last = start[experts - 1] + (total[experts - 1] + align - 1) / align * align;
+    for (uint32_t r = last + block * kSortThreads + tid; r < rows; r += blocks * kSortThreads)
+        src[r] = -1;
+}
+
+// ----------------------------------------------------------------------------
+// Rows of a list of elements
+// ----------------------------------------------------------------------------
+
+enum { kElemBF16 = 0, kElemF16 = 1, kElemF32 = 2 };
+
+template <int DT> struct Elem { typedef uint16_t type; static constexpr uint32_t vec = 8; };
+template <> struct Elem<kElemF32> { typedef float type; static constexpr uint32_t vec = 4; };
+
+template <int DT> __device__ __forceinline__ float elem_to_f32(typename Elem<DT>::type v)
+{
+    if constexpr (DT == kElemF32)
+        return v;
+    else if constexpr (DT == kElemBF16)
+        return __uint_as_float((uint32_t)v << 16);
+    else
+        return (float)__builtin_bit_cast(_Float16, v);
+}
+
+// One rounding, to nearest even; a NaN stays a NaN.
+template <int DT> __device__ __forceinline__ typename Elem<DT>::type elem_from_f32(float v)
+{
+    if constexpr (DT == kElemF32)
+        return v;
+    else if constexpr (DT == kElemBF16)
+        return __builtin_bit_cast(uint16_t, (__bf16)v);
+    else
+        return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+// 16 bytes of a row at element alignment: rows of any length start anywhere,
+// and the memory path takes 16-byte accesses at any element boundary.
+template <int DT> struct __attribute__((packed, aligned(sizeof(typename Elem<DT>::type)))) ElemVec {
+    typename Elem<DT>::type v[Elem<DT>::vec];
+};
+
+// `n` (1 .. vec) elements at p as f32; elements past n are zero.
+template <int DT> __device__ __forceinline__ void load_elems(const typename Elem<DT>::type *p, uint32_t n, float *f)
+{
+    constexpr uint32_t V = Elem<DT>::vec;
+    if (n >= V) {
+        const ElemVec<DT> t = *reinterpret_cast<const ElemVec<DT> *>(p);
+#pragma unroll
+        for (uint32_t i = 0; i < V; i++)
+            f[i] = elem_to_f32<DT>(t.v[i]);
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < V; i++)
+            f[i] = i < n ? elem_to_f32<DT>(p[i]) : 0.0f;
+    }
+}
+
+template <int DT> __device__ __forceinline__ void store_elems(typename Elem<DT>::type *p, uint32_t n, const float *f)
+{
+    constexpr uint32_t V = Elem<DT>::vec;
+    if (n >= V) {
+        ElemVec<DT> t;
+#pragma unroll
+        for (uint32_t i = 0; i < V; i++)
+            t.v[i] = elem_from_f32<DT>(f[i]);
+        *reinterpret_cast<ElemVec<DT> *>(p) = t;
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < V; i++)
+            if (i < n)
+                p[i] = elem_from_f32<DT>(f[i]);
+    }
+}
+
+// ----------------------------------------------------------------------------
+// Combine: out[t] = sum over j of w[t][j] * y[dest[t][j]]
+// ----------------------------------------------------------------------------
+//
+// A thread owns 16 bytes of one token's result row and adds the slots in
+// order in f32, rounding once: the result does not depend on the launch. A
+// dest outside [0, rows) adds nothing, whatever its weight; a token none of
+// whose pairs has a row gets zeros.
+template <int DT, int WEIGHTED>
+__global__ __launch_bounds__(256) void combine_kernel(const typename Elem<DT>::type *__restrict__ y, uint32_t rows,
+                                                      uint32_t N, uint32_t vecs, const int32_t *__restrict__ dest,
+                                                      const float *__restrict__ weights, uint32_t tokens,
+                                                      uint32_t slots, typename Elem<DT>::type *__restrict__ out)
+{
+    constexpr uint32_t V = Elem<DT>::vec;
+    const uint64_t n = (uint64_t)blockIdx.x * 256u + threadIdx.x;
+    const uint64_t t = n / vecs;
+    if (t >= tokens)
+        return;
+    const uint32_t c = (uint32_t)(n - t * vecs) * V;
+    const uint32_t left = N - c;
+    float acc[V] = {};
+    for (uint32_t j = 0; j < slots; j++) {
+        const uint32_t r = (uint32_t)dest[t * slots + j];
+        if (r >= rows)
+            continue;
+        const float w = WEIGHTED ? weights[t * slots + j] : 1.0f;
+        float f[V];
+        load_elems<DT>(y + (uint64_t)r * N + c, left, f);
+#pragma unroll
+        for (uint32_t i = 0; i < V; i++)
+            acc[i] = WEIGHTED ? __builtin_fmaf(w, f[i], acc[i]) : acc[i] + f[i];
+    }
+    store_elems<DT>(out + t * N + c, left, acc);
+}
+
+// ----------------------------------------------------------------------------
+// The gradient of combine
+// ----------------------------------------------------------------------------
+//
+//   grad_y[r]    = w[src[r]] * grad[src[r] / slots], zero for a row without a pair
+//   grad_w[t][j] = sum over n of grad[t][n] * y[dest[t][j]][n], zero for a pair
+//                  without a row
+//
+// `WAVES` waves take one token: its gradient row is read once for kBackSlots
+// slots at a time, each slot's y row is read and its grad_y row written in
+// the same pass, and the products' sums stay in registers until one reduction
+// per slot (in a fixed order). Workgroups past the tokens' own clear the rows
+// that no pair has.
+constexpr uint32_t kBackSlots = 8;
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+template <int DT, int WAVES>
+__global__ __launch_bounds__(256) void combine_backward_kernel(
+    const typename Elem<DT>::type *__restrict__ grad, const typename Elem<DT>::type *__restrict__ y, uint32_t rows,
+    uint32_t N, const int32_t *__restrict__ src, const int32_t *__restrict__ dest, const float *__restrict__ weights,
+    uint32_t tokens, uint32_t slots, uint32_t token_blocks, typename Elem<DT>::type *__restrict__ grad_y,
+    float *__restrict__ grad_w)
+{
+    constexpr uint32_t V = Elem<DT>::vec, PER = 4 / WAVES;   // tokens per workgroup
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    if (blockIdx.x >= token_blocks) {
+        const uint32_t r0 = (blockIdx.x - token_blocks) * 256u + wave * 64u;
+        const uint32_t r = r0 + lane;
+        const bool empty = r < rows && (uint32_t)src[r] >= (uint64_t)tokens * slots;
+        const float zero[V] = {};
+        for (uint64_t m = __ballot(empty); m; m &= m - 1) {
+            const uint64_t row = r0 + (uint32_t)__builtin_ctzll(m);
+            for (uint32_t c = lane * V; c < N; c += 64 * V)
+                store_elems<DT>(grad_y + row * N + c, N - c, zero);
+        }
+        return;
+    }
+
+    __shared__ float sums[4][kBackSlots];
+    const uint32_t t = blockIdx.x * PER + wave / WAVES;
+    const uint32_t first = (wave % WAVES * 64u + lane) * V;
+    for (uint32_t j0 = 0; j0 < slots; j0 += kBackSlots) {
+        uint32_t r[kBackSlots];
+        float w[kBackSlots], acc[kBackSlots];
+#pragma unroll
+        for (uint32_t j = 0; j < kBackSlots; j++) {
+            const bool has = t < tokens && j0 + j < slots;
+            r[j] = has ? (uint32_t)dest[(uint64_t)t * slots + j0 + j] : ~0u;
+            w[j] = has ? weights[(uint64_t)t * slots + j0 + j] : 0.0f;
+            acc[j] = 0.0f;
+        }
+        if (t < tokens) {
+            for (uint32_t c = first; c < N; c += WAVES * 64 * V) {
+                float g[V];
+                load_elems<DT>(grad + (uint64_t)t * N + c, N - c, g);
+#pragma unroll
+                for (uint32_t j = 0; j < kBackSlots; j++) {
+                    if (r[j] >= rows)
+                        continue;
+                    float f[V], o[V];
+                    load_elems<DT>(y + (uint64_t)r[j] * N + c, N - c, f);
+#pragma unroll
+                    for (uint32_t i = 0; i < V; i++) {
+                        acc[j] = __builtin_fmaf(g[i], f[i], acc[j]);
+                        o[i] = w[j] * g[i];
+                    }
+                    store_elems<DT>(grad_y + (uint64_t)r[j] * N + c, N - c, o);
+                }
+            }
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < kBackSlots; j++)
+            acc[j] = wave_sum(acc[j]);
+        if constexpr (WAVES > 1) {
+            __syncthreads();   // the previous slots' sums have been read
+            if (lane == 0)
+#pragma unroll
+                for (uint32_t j = 0; j < kBackSlots; j++)
+                    sums[wave][j] = acc[j];
+            __syncthreads();
+            if (wave == 0 && lane < kBackSlots && t < tokens && j0 + lane < slots) {
+                float s = 0.0f;
+#pragma unroll
+                for (uint32_t k = 0; k < WAVES; k++)
+                    s += sums[k][lane];
+                grad_w[(uint64_t)t * slots + j0 + lane] = s;
+            }
+        } else if (t < tokens) {
+#pragma unroll
+            for (uint32_t j = 0; j < kBackSlots; j++)
+                if (lane == j && j0 + j < slots)
+                    grad_w[(uint64_t)t * slots + j0 + j] = acc[j];
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------
+// Gather and quantize
+// ----------------------------------------------------------------------------
+//
+// The quantize of the [rows, K] tensor whose row r is x[src[r] / slots] (zeros
+// where src[r] is no pair), with blocks along its rows (the along kernel's
+// tile, lane mapping and LDS transpose, see mxq_axis_kernels.hpp) or down its
+// columns (the down kernel's). The row numbers are the only difference in
+// what is read; the result bytes are those of quantize_axis on that tensor.
+
+// Token of sorted row r, or -1.
+__device__ __forceinline__ int32_t row_token(const int32_t *src, uint32_t r, uint32_t rows, uint32_t pairs,
+                                             uint32_t slots)
+{
+    const uint32_t s = r < rows ? (uint32_t)src[r] : ~0u;
+    return s < pairs ? (int32_t)(s / slots) : -1;
+}
+
+template <int IN, int OUT>
+__global__ __launch_bounds__(64 * kAlongWaves) void gather_quantize_along_kernel(
+    const uint16_t *__restrict__ x, const int32_t *__restrict__ src, uint32_t rows, uint32_t pairs, uint32_t slots,
+    uint64_t K, uint32_t tiles_m, int emax_bias, uint32_t dense, uint8_t *__restrict__ data,
+    uint8_t *__restrict__ scale)
+{
+    constexpr uint32_t RT = kAlongRows, KG = kAlongWaveRows / 32;
+    constexpr uint32_t CB = OUT == kOutE2M1 ? 2 : 4;
+    constexpr uint32_t PITCH = RT * CB + 16;
+    __shared__ __attribute__((aligned(16))) uint8_t codes[16 * PITCH];
+    __shared__ __attribute__((aligned(16))) uint8_t e8m0[2 * RT];
+    __shared__ int32_t token[RT];
+
+    const uint32_t t = threadIdx.x, w = t >> 6, l = t & 63u;
+    const uint32_t c = l & 7u, i = l >> 3, q = c & 3u, bl = c >> 2;
+    const uint32_t tk = blockIdx.x / tiles_m;
+    const uint32_t m0 = (blockIdx.x - tk * tiles_m) * RT;
+    const uint32_t G = (uint32_t)(K / 32);
+    const uint32_t g = tk * 2u + bl;
+
+    for (uint32_t r = t; r < RT; r += 64 * kAlongWaves)
+        token[r] = row_token(src, m0 + r, rows, pairs, slots);
+    __syncthreads();
+
+    u32x4_t v[4 * KG];
+#pragma unroll
+    for (uint32_t k = 0; k < 4 * KG; k++) {
+        const int32_t tok = token[kAlongWaveRows * w + 4u * i + (k & 3u) + 32u * (k >> 2)];
+        const bool ok = g < G && tok >= 0;
+        v[k] = *reinterpret_cast<const u32x4_t *>(x + (ok ? (uint64_t)tok * K + g * 32u : 0u) + 8u * q);
+        v[k] = ok ? v[k] : u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (uint32_t kg = 0; kg < KG; kg++) {
+        uint32_t lo[4], hi[4], eb[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const u32x4_t a = v[4 * kg + j];
+            uint32_t mm = pk_max_u16(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu);
+            mm = pk_max_u16(mm, a.z & 0x7FFF7FFFu);
+            mm = pk_max_u16(mm, a.w & 0x7FFF7FFFu);
+            const uint32_t mag = quad_max(max(mm & 0xFFFFu, mm >> 16));
+            uint32_t e[1] = {block_e8m0<IN>(mag, emax_bias)};
+            const float s = e8m0_to_scale(e[0]);
+            uint32_t w0[2] = {a.x, a.y}, w1[2] = {a.z, a.w};
+            uint32_t o0[1], o1[1];
+            if constexpr (OUT == kOutE2M1) {
+                o0[0] = fp4_container<IN, 0>(0u, w0[0], w0[1], s);
+                o1[0] = fp4_container<IN, 0>(0u, w1[0], w1[1], s);
+            } else {
+                o0[0] = fp8x4<IN, OUT>(w0[0], w0[1], s);
+                o1[0] = fp8x4<IN, OUT>(w1[0], w1[1], s);
+            }
+            if (mag > InfBits<IN>::value || e[0] == 254u) {
+                fix_special_codes<IN, OUT, 1>(w0, e, o0);
+                fix_special_codes<IN, OUT, 1>(w1, e, o1);
+            }
+            lo[j] = o0[0];
+            hi[j] = o1[0];
+            eb[j] = e[0];
+        }
+        const uint32_t r = kAlongWaveRows * w + 4u * i + 32u * kg;
+        uint8_t *s0 = codes + (8u * bl + 2u * q) * PITCH + CB * r;
+        if constexpr (OUT == kOutE2M1) {
+            *reinterpret_cast<u32x2_t *>(s0) = u32x2_t{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
+            *reinterpret_cast<u32x2_t *>(s0 + PITCH) = u32x2_t{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
+        } else {
+            *reinterpret_cast<u32x4_t *>(s0) = u32x4_t{lo[0], lo[1], lo[2], lo[3]};
+            *reinterpret_cast<u32x4_t *>(s0 + PITCH) = u32x4_t{hi[0], hi[1], hi[2], hi[3]};
+        }
+        if (q == 0)
+            *reinterpret_cast<uint32_t *>(e8m0 + bl * RT + r) = eb[0] | eb[1] << 8 | eb[2] << 16 | eb[3] << 24;
+    }
+    __syncthreads();
+
+    // `rows` is a multiple of 4 (checked on the host): 4 rows per lane
+    using T = typename std::conditional<OUT == kOutE2M1, u32x2_t, u32x4_t>::type;
+    constexpr uint32_t VPW = 16 / kAlongWaves, SPR = RT / 256;
+    T val[VPW][SPR];
+#pragma unroll
+    for (uint32_t j = 0; j < VPW; j++)
+#pragma unroll
+        for (uint32_t s = 0; s < SPR; s++)
+            val[j][s] = *reinterpret_cast<const T *>(codes + (VPW * w + j) * PITCH + CB * (256u * s + 4u * l));
+#pragma unroll
+    for (uint32_t j = 0; j < VPW; j++) {
+        const uint32_t vr = VPW * w + j;
+        const uint64_t p = (uint64_t)tk * 16u + vr;
+#pragma unroll
+        for (uint32_t s = 0; s < SPR; s++) {
+            const uint32_t r = 256u * s + 4u * l;
+            if (tk * 2u + (vr >> 3) < G && m0 + r < rows)
+                store<1>(reinterpret_cast<T *>(data + (p * rows + m0 + r) * CB), val[j][s]);
+        }
+    }
+    for (uint32_t idx = t; idx < 2 * RT / 4; idx += 64 * kAlongWaves) {
+        const uint32_t strip = idx / (RT / 4), r = 4u * (idx - strip * (RT / 4));
+        const uint32_t gg = tk * 2u + strip;
+        if (gg < G && m0 + r < rows) {
+            const uint64_t slot = dense ? gg : (gg & 3u) + 32ull * (gg >> 2);
+            store<1>(reinterpret_cast<uint32_t *>(scale + slot * rows + m0 + r),
+                     *reinterpret_cast<const uint32_t *>(e8m0 + strip * RT + r));
+        }
+    }
+}
+
+// Blocks of 32 sorted rows (rows % 32 == 0, groups aligned to 32: no block
+// spans two experts). Lane r < 32 looks up row r's token, and every lane gets
+// all 32 of them in scalar registers before the lanes past the tensor leave.
+template <int IN, int OUT, int NB>
+__global__ __launch_bounds__(64) void gather_quantize_down_kernel(const uint16_t *__restrict__ x,
+                                                                  const int32_t *__restrict__ src, uint32_t rows,
+                                                                  uint32_t pairs, uint32_t slots, uint64_t N,
+                                                                  uint32_t nstrips, uint32_t tiles_per_band,
+                                                                  int emax_bias, uint32_t dense,
+                                                                  uint8_t *__restrict__ data,
+                                                                  uint8_t *__restrict__ scale)
+{
+    constexpr int NW = (NB + 1) / 2;
+    constexpr uint32_t LANE_BYTES = OUT == kOutE2M1 ? 2 * NB : 4 * NB;
+    const uint32_t band = blockIdx.x / tiles_per_band;
+    const uint32_t strip = (blockIdx.x - band * tiles_per_band) * 64u + threadIdx.x;
+    const int32_t mine = row_token(src, band * 32u + (threadIdx.x & 31u), rows, pairs, slots);
+    int32_t token[32];
+#pragma unroll
+    for (int r = 0; r < 32; r++)
+        token[r] = __builtin_amdgcn_readlane(mine, r);
+    if (strip >= nstrips)
+        return;
+    const uint64_t n0 = (uint64_t)strip * NB;
+    uint32_t v[32][NW];
+#pragma unroll
+    for (int r = 0; r < 32; r++) {
+        const int32_t tok = token[r];
+        const uint16_t *p = x + (uint64_t)(tok < 0 ? 0 : tok) * N + n0;
+        if constexpr (NB == 4) {
+            const u32x2_t d = *reinterpret_cast<const u32x2_t *>(p);
+            v[r][0] = tok < 0 ? 0u : d.x;
+            v[r][1] = tok < 0 ? 0u : d.y;
+        } else if constexpr (NB == 2) {
+            v[r][0] = tok < 0 ? 0u : *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            v[r][0] = tok < 0 ? 0u : *p;
+        }
+    }
+
+    uint32_t e[NB];
+    float s[NB];
+    bool special = false;
+#pragma unroll
+    for (int h = 0; h < NW; h++) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < 32; r++)
+            m = pk_max_u16(m, v[r][h] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int q = 0; q < 2 && 2 * h + q < NB; q++) {
+            const uint32_t mag = half16(m, q);
+            e[2 * h + q] = block_e8m0<IN>(mag, emax_bias);
+            s[2 * h + q] = e8m0_to_scale(e[2 * h + q]);
+            special |= mag > InfBits<IN>::value || e[2 * h + q] == 254u;
+        }
+    }
+    constexpr int OW = OUT == kOutE2M1 ? NW : NB;
+    uint32_t out[8][OW];
+#pragma unroll
+    for (int pr = 0; pr < 8; pr++) {
+        uint32_t w[2 * NB];
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+            const int h = b / 2, q = b & 1;
+            w[2 * b] = half16(v[4 * pr][h], q) | half16(v[4 * pr + 1][h], q) << 16;
+            w[2 * b + 1] = half16(v[4 * pr + 2][h], q) | half16(v[4 * pr + 3][h], q) << 16;
+        }
+        if constexpr (OUT == kOutE2M1) {
+#pragma unroll
+            for (int h = 0; h < NW; h++) {
+                out[pr][h] = fp4_container<IN, 0>(0u, w[4 * h], w[4 * h + 1], s[2 * h]);
+                if constexpr (NB > 1)
+                    out[pr][h] = fp4_container<IN, 1>(out[pr][h], w[4 * h + 2], w[4 * h + 3], s[2 * h + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < NB; b++)
+                out[pr][b] = fp8x4<IN, OUT>(w[2 * b], w[2 * b + 1], s[b]);
+        }
+        if (special)
+            fix_special_codes<IN, OUT, NB>(w, e, out[pr]);
+    }
+#pragma unroll
+    for (int pr = 0; pr < 8; pr++)
+        store_bytes<LANE_BYTES, 1>(data + ((uint64_t)band * 8u + pr) * N * (LANE_BYTES / NB) +
+                                       n0 * (LANE_BYTES / NB), out[pr]);
+    const uint64_t slot = dense ? (uint64_t)band : (uint64_t)(band & 3u) + 32u * (uint64_t)(band >> 2);
+    uint32_t packed[1] = {0};
+#pragma unroll
+    for (int b = 0; b < NB; b++)
+        packed[0] |= e[b] << (8 * b);
+    store_bytes<NB, 1>(scale + slot * N + n0, packed);
+}
+
+} // namespace mxq

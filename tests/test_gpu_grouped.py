@@ -1,0 +1,298 @@
+"""GPU tests of the experts' products on MX operands against exact (64-bit) sums.
+
+The matrix cores add the 32 products of a scale block in fixed point with
+about 13 fraction bits below the largest of them and combine blocks in fp32,
+so, as for the scaled matmul,
+    |gpu - exact| <= sum over blocks of 31 * 2^-12 * max|l| max|r|
+                     + (adds + 2) * 2^-24 * sum|l r|
+and a bf16 result is off by half a step (2^-8) of that more. `adds` counts the
+fp32 additions: one per block, up to four under a scale byte of 255, and up to
+16 where waves share the contraction.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mx_microscaling_quantization_amd as mxq
+import oracle
+import workloads
+from conftest import progress
+
+pytestmark = pytest.mark.gpu
+
+FP32_OVERFLOW = (2.0 - 2.0 ** -24) * 2.0 ** 127
+
+
+def values(codes, scale, fmt):
+    """[K, C] float64 of codes [P, 4C] and dense scales [P/8, C]."""
+    P, C = codes.shape[0], scale.shape[1]
+    v = oracle.decode(codes, fmt).reshape(P, C, 4).transpose(0, 2, 1).reshape(4 * P, C)
+    return v * np.ldexp(1.0, np.repeat(scale.astype(np.int64), 32, axis=0) - 127)
+
+
+def quantized(R, C, dim, fmt, seed):
+    bits = workloads.random_bits(R, C, "bf16", seed=seed)
+    return oracle.quantize_axis(bits, "bf16", fmt, dim, layout="dense")
+
+
+def product(L, R):
+    with np.errstate(invalid="ignore", over="ignore"):
+        return L.T @ R
+
+
+def bound(L, R, want, res, per_block=1):
+    K = L.shape[0]
+    with np.errstate(invalid="ignore", over="ignore"):
+        aL, aR = np.abs(L), np.abs(R)
+        mL, mR = aL.reshape(K // 32, 32, -1).max(1), aR.reshape(K // 32, 32, -1).max(1)
+        tol = 31 * 2.0 ** -12 * (mL.T @ mR) + (per_block * (K // 32) + 18) * 2.0 ** -24 * (aL.T @ aR)
+        if res == torch.bfloat16:
+            tol = tol + 2.0 ** -8 * (np.abs(want) + tol)
+    return np.nan_to_num(tol, nan=0.0)
+
+
+def compare(got, L, R, res, per_block=1):
+    """Against the exact product. Where the terms' magnitudes add up to more
+    than fp32 holds, a partial sum may overflow either way, so a result there is
+    determined only if the terms of the other sign cannot overflow."""
+    want = product(L, R)
+    tol = bound(L, R, want, res, per_block)
+    mags = product(np.abs(L), np.abs(R))
+    nan = np.isnan(want)
+    over = ~nan & (mags >= FP32_OVERFLOW)
+    assert np.array_equal(np.isnan(got) & ~over, nan), "NaN in other places"
+    other = (mags - np.abs(want)) / 2      # the terms of the other sign
+    one_sign = over & (np.abs(want) >= 2 * FP32_OVERFLOW) & (other < FP32_OVERFLOW / 2)
+    assert np.array_equal(got[one_sign], np.copysign(np.inf, want[one_sign]))
+    fin = ~nan & ~over
+    bad = np.argwhere(fin & ~(np.abs(got - want) <= tol))
+    assert bad.size == 0, "%d outside; first %s: %r for %r, bound %r" % (
+        len(bad), bad[0], got[tuple(bad[0])], want[tuple(bad[0])], tol[tuple(bad[0])])
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def check_rows(sizes, tail, K, N, fmt, res, seed=0, patch=None, per_block=1):
+    """Groups of these sizes and `tail` rows past the last one."""
+    offsets = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    rows, G = int(offsets[-1]) + tail, len(sizes)
+    l, ls = quantized(rows, K, -1, fmt, seed + rows + K)
+    r, rs = (np.stack(t) for t in zip(*[quantized(K, N, -2, fmt, seed + 77 * g + N) for g in range(G)]))
+    if patch:
+        patch(l, ls, r, rs)
+    out = torch.full((rows, N), 7.0, dtype=res, device="cuda")
+    mxq.grouped_scaled_matmul(dev(l), dev(ls), dev(r), dev(rs), dev(offsets), fmt, res, out=out)
+    got = host(out)
+    L = values(l, ls, fmt)
+    for g in range(G):
+        a, b = offsets[g], offsets[g + 1]
+        if a == b:
+            continue
+        compare(got[a:b], L[:, a:b], values(r[g], rs[g], fmt), res, per_block)
+    assert (got[offsets[-1]:] == 0).all(), "rows past the last group"
+
+
+# mean rows per group (rows / groups) pick the tile: 32 rows, 64 rows, 256 rows
+GROUPINGS = [([4], 0), ([32], 0), ([0, 0, 0], 32), ([4, 0, 36, 32], 12), ([32] * 9, 64), ([40, 8, 0, 100], 0),
+             ([64, 64, 128], 0), ([100, 60, 92, 0, 128], 20), ([256], 0), ([260, 512, 4], 0), ([0, 700, 124], 36)]
+
+
+@pytest.mark.parametrize("fmt,res", [("e4m3fn", torch.bfloat16), ("e4m3fn", torch.float32), ("e5m2", torch.bfloat16),
+                                     ("e5m2", torch.float32)])
+@pytest.mark.parametrize("sizes,tail", GROUPINGS)
+def test_rows(sizes, tail, fmt, res):
+    progress("grouped rows %s tail %d %s %s" % (sizes, tail, fmt, res))
+    check_rows(sizes, tail, 128, 132, fmt, res)
+
+
+@pytest.mark.parametrize("K,N", [(32, 4), (32, 128), (64, 8), (96, 60), (160, 260), (672, 300), (1056, 516)])
+@pytest.mark.parametrize("sizes", [[8, 24, 0, 44], [72, 56, 90 * 4 - 128], [300, 212]])
+def test_rows_sizes(sizes, K, N):
+    progress("grouped rows %s K=%d N=%d" % (sizes, K, N))
+    check_rows(sizes, 8, K, N, "e4m3fn", torch.bfloat16, seed=3)
+
+
+def test_rows_many_groups():
+    """More groups than lanes of a wave, most of them empty or small."""
+    g = np.random.default_rng(2)
+    for G in (64, 65, 200, 1024):
+        sizes = 4 * g.integers(0, 6, size=G) * (g.random(G) < 0.4)
+        progress("grouped rows, %d groups" % G)
+        check_rows(sizes.tolist(), 40, 64, 36, "e4m3fn", torch.bfloat16, seed=G)
+
+
+def test_rows_many_tiles():
+    """Tiles past the walk of four tile rows and past the XCDs' shares."""
+    progress("grouped rows, 256-row tiles, 7 x 5 tiles")
+    check_rows([516, 0, 1028], 300, 96, 1160, "e5m2", torch.bfloat16)
+    progress("grouped rows, 32-row tiles")
+    check_rows([36] * 23, 100, 96, 516, "e4m3fn", torch.float32)
+
+
+def test_no_contraction_is_zero():
+    z = torch.zeros((0, 4 * 64), dtype=torch.uint8, device="cuda")
+    zs = torch.zeros((0, 64), dtype=torch.uint8, device="cuda")
+    r, rs = torch.zeros((2, 0, 32), dtype=torch.uint8, device="cuda"), torch.zeros((2, 0, 8), dtype=torch.uint8, device="cuda")
+    off = torch.tensor([0, 32, 64], dtype=torch.int32, device="cuda")
+    out = torch.full((64, 8), 5.0, device="cuda")
+    mxq.grouped_scaled_matmul(z, zs, r, rs, off, "e4m3fn", torch.float32, out=out)
+    assert int(torch.count_nonzero(out)) == 0
+    out = torch.full((2, 64, 64), 5.0, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    mxq.grouped_scaled_matmul_wgrad(z, zs, z, zs, off, "e4m3fn", torch.float32, out=out)
+    assert int(torch.count_nonzero(out)) == 0
+
+
+@pytest.mark.parametrize("sizes", [[32, 64], [64, 96], [256, 320]])
+@pytest.mark.parametrize("res", [torch.float32, torch.bfloat16])
+def test_rows_scale_255(sizes, res):
+    """A scale byte of 255 stands for 2^128, on either side."""
+    def left(l, ls, r, rs):
+        ls[1, 3:9] = 255
+        rs[:, 1, :] = 20
+
+    def both(l, ls, r, rs):
+        ls[2, ::3] = 255
+        ls[2, 1::3] = 120
+        rs[:, 2, ::2] = 255
+        rs[:, 2, 1::2] = 30
+        rs[:, 0, 5] = 255
+        ls[0, :] = 10
+
+    progress("grouped rows with scale 255 %s %s" % (sizes, res))
+    check_rows(sizes, 4, 160, 132, "e4m3fn", res, patch=left, per_block=4)
+    check_rows(sizes, 4, 160, 132, "e5m2", res, patch=both, per_block=4)
+
+
+@pytest.mark.parametrize("sizes", [[32, 64], [64, 96], [256, 320]])
+def test_rows_nan_stays_in_its_row(sizes):
+    def patch(l, ls, r, rs):
+        l[2, 4 * 5 + 1] = 0x7F          # row 5 of the sorted rows
+        r[1, 3, 4 * 7] = 0xFF           # column 7 of group 1
+
+    check_rows(sizes, 0, 96, 64, "e4m3fn", torch.float32, patch=patch, per_block=4)
+
+
+@pytest.mark.parametrize("sizes,M,N", [([32], 4, 4), ([32, 0, 64], 64, 36), ([96, 160, 0, 32], 256, 256),
+                                       ([0, 0], 12, 20), ([128, 32], 260, 516), ([32] * 20, 100, 132), ([1056], 132, 64)])
+@pytest.mark.parametrize("fmt,res", [("e4m3fn", torch.bfloat16), ("e5m2", torch.float32)])
+def test_wgrad(sizes, M, N, fmt, res):
+    progress("grouped wgrad %s M=%d N=%d %s %s" % (sizes, M, N, fmt, res))
+    offsets = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    rows, G = int(offsets[-1]) + 64, len(sizes)
+    l, ls = quantized(rows, M, -2, fmt, M + rows)
+    r, rs = quantized(rows, N, -2, fmt, N + rows + 1)
+    out = torch.full((G, M, N), 7.0, dtype=res, device="cuda")
+    mxq.grouped_scaled_matmul_wgrad(dev(l), dev(ls), dev(r), dev(rs), dev(offsets), fmt, res, out=out)
+    got, L, R = host(out), values(l, ls, fmt), values(r, rs, fmt)
+    for g in range(G):
+        a, b = offsets[g], offsets[g + 1]
+        if a == b:
+            assert (got[g] == 0).all()
+            continue
+        compare(got[g], L[a:b], R[a:b], res)
+
+
+def test_wgrad_scale_255_stays_in_its_group():
+    sizes, M, N = [64, 96, 32], 132, 68
+    offsets = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    rows = int(offsets[-1])
+    l, ls = quantized(rows, M, -2, "e4m3fn", 5)
+    r, rs = quantized(rows, N, -2, "e4m3fn", 6)
+    ls[3, ::5], rs[3, :] = 255, 25      # block 3: in group 1
+    out = mxq.grouped_scaled_matmul_wgrad(dev(l), dev(ls), dev(r), dev(rs), dev(offsets), "e4m3fn", torch.float32)
+    got, L, R = host(out), values(l, ls, "e4m3fn"), values(r, rs, "e4m3fn")
+    for g in range(3):
+        a, b = offsets[g], offsets[g + 1]
+        compare(got[g], L[a:b], R[a:b], torch.float32, 4)
+
+
+def test_gradients_against_differences():
+    """Small whole numbers are exact in e4m3 blocks and in the products, so a
+    difference of the loss sum(G * (X @ W)) in one weight or one input is the
+    gradient exactly."""
+    g = np.random.default_rng(4)
+    sizes = [32, 0, 64]
+    offsets = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    K, N, rows = 64, 32, 96
+    X, G = g.integers(-4, 5, size=(rows, K)), g.integers(-4, 5, size=(rows, N))
+    W = g.integers(-4, 5, size=(3, K, N))
+    off = dev(offsets)
+
+    def quant(a, dim):
+        return mxq.quantize_axis(torch.from_numpy(a).to(torch.bfloat16).cuda(), "e4m3fn", dim, dense_scale=True)
+
+    def stack(W, dim):
+        return tuple(torch.stack(t) for t in zip(*[quant(w, dim) for w in W]))
+
+    def loss(X, W):
+        out = mxq.grouped_scaled_matmul(*quant(X, -1), *stack(W, -2), off, "e4m3fn", torch.float32)
+        return float((out.double().cpu().numpy() * G).sum())
+
+    dX = mxq.grouped_scaled_matmul(*quant(G, -1), *stack(W, -1), off, "e4m3fn", torch.float32).cpu().numpy()
+    dW = mxq.grouped_scaled_matmul_wgrad(*quant(X, -2), *quant(G, -2), off, "e4m3fn", torch.float32).cpu().numpy()
+    for e, k, n in [(0, 0, 0), (2, 63, 31), (2, 17, 5), (1, 3, 3)]:
+        p, m = W.copy(), W.copy()
+        p[e, k, n] += 1
+        m[e, k, n] -= 1
+        assert (loss(X, p) - loss(X, m)) / 2 == dW[e, k, n]
+    for r, k in [(0, 0), (31, 63), (32, 7), (95, 40)]:
+        p, m = X.copy(), X.copy()
+        p[r, k] += 1
+        m[r, k] -= 1
+        assert (loss(p, W) - loss(m, W)) / 2 == dX[r, k]
+
+
+def test_offsets_out_of_range_are_clamped():
+    """Offsets that run past the rows or back: no access out of bounds, and the
+    groups that are sensible have their results."""
+    K, N, rows = 64, 64, 128
+    l, ls = quantized(rows, K, -1, "e4m3fn", 1)
+    r, rs = (np.stack(t) for t in zip(*[quantized(K, N, -2, "e4m3fn", g) for g in range(4)]))
+    for off in ([0, 32, 64, 4096, 2 ** 31 - 4], [-64, 32, 16, 64, 96], [2 ** 31 - 4] * 5, [-4] * 5):
+        out = mxq.grouped_scaled_matmul(dev(l), dev(ls), dev(r), dev(rs), dev(np.array(off, np.int32)), "e4m3fn",
+                                        torch.float32)
+        torch.cuda.synchronize()
+        if off[0] <= 0 and off[1] == 32:   # rows 0 .. 15 are only group 0's in both lists
+            compare(host(out)[:16], values(l, ls, "e4m3fn")[:, :16], values(r[0], rs[0], "e4m3fn"), torch.float32)
+        x, xs = quantized(rows, 64, -2, "e4m3fn", 9)
+        mxq.grouped_scaled_matmul_wgrad(dev(x), dev(xs), dev(x), dev(xs), dev(np.array(off, np.int32)), "e4m3fn",
+                                        torch.float32)
+        torch.cuda.synchronize()
+
+
+def test_other_stream_graph_and_repeats():
+    sizes = [32, 96, 0, 64]
+    off = dev(np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32))
+    l, ls = map(dev, quantized(192, 128, -1, "e4m3fn", 1))
+    r, rs = (dev(np.stack(t)) for t in zip(*[quantized(128, 132, -2, "e4m3fn", g) for g in range(4)]))
+    x, xs = map(dev, quantized(192, 64, -2, "e4m3fn", 2))
+    want = mxq.grouped_scaled_matmul(l, ls, r, rs, off)
+    want_w = mxq.grouped_scaled_matmul_wgrad(x, xs, x, xs, off)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        a = mxq.grouped_scaled_matmul(l, ls, r, rs, off, stream=s)
+        b = mxq.grouped_scaled_matmul_wgrad(x, xs, x, xs, off, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(a, want) and torch.equal(b, want_w)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a = mxq.grouped_scaled_matmul(l, ls, r, rs, off)
+        b = mxq.grouped_scaled_matmul_wgrad(x, xs, x, xs, off)
+    for _ in range(4):
+        a.zero_()
+        b.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, want_w)
+        _ = (a.float() * 2).sum().item()
