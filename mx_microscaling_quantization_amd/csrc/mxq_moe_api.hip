@@ -82,10 +82,10 @@ int sort_launch(const void *ids_, int64_t pairs, int64_t experts, int64_t align,
 
 // ---- gather and quantize ---------------------------------------------------
 
-typedef void (*along_fn)(const uint16_t *, const int32_t *, uint32_t, uint32_t, uint32_t, uint64_t, uint32_t, int,
-                         uint32_t, uint8_t *, uint8_t *);
-typedef void (*down_fn)(const uint16_t *, const int32_t *, uint32_t, uint32_t, uint32_t, uint64_t, uint32_t, uint32_t,
-                        int, uint32_t, uint8_t *, uint8_t *);
+typedef void (*along_fn)(const uint16_t *, const int32_t *, uint32_t, uint32_t, uint32_t, uint32_t, uint64_t, uint32_t,
+                         int, uint32_t, uint8_t *, uint8_t *);
+typedef void (*down_fn)(const uint16_t *, const int32_t *, uint32_t, uint32_t, uint32_t, uint32_t, uint64_t, uint32_t,
+                        uint32_t, int, uint32_t, uint8_t *, uint8_t *);
 
 template <int IN> along_fn along_pick(int out)
 {
@@ -96,25 +96,43 @@ template <int IN> along_fn along_pick(int out)
     }
 }
 
-template <int IN, int OUT> down_fn down_pick_nb(int nb)
+template <int IN, int OUT> down_fn down_pick_nb(int nb, bool runs)
 {
     switch (nb) {
-    case 4: return mxq::gather_quantize_down_kernel<IN, OUT, 4>;
-    case 2: return mxq::gather_quantize_down_kernel<IN, OUT, 2>;
-    default: return mxq::gather_quantize_down_kernel<IN, OUT, 1>;
+    case 4: return runs ? mxq::gather_quantize_down_kernel<IN, OUT, 4, 1>
+                        : mxq::gather_quantize_down_kernel<IN, OUT, 4, 0>;
+    case 2: return mxq::gather_quantize_down_kernel<IN, OUT, 2, 0>;
+    default: return mxq::gather_quantize_down_kernel<IN, OUT, 1, 0>;
     }
 }
 
-template <int IN> down_fn down_pick(int out, int nb)
+template <int IN> down_fn down_pick(int out, int nb, bool runs)
 {
     switch (out) {
-    case MXQ_OUT_E4M3FN: return down_pick_nb<IN, mxq::kOutE4M3FN>(nb);
-    case MXQ_OUT_E5M2: return down_pick_nb<IN, mxq::kOutE5M2>(nb);
-    default: return down_pick_nb<IN, mxq::kOutE2M1>(nb);
+    case MXQ_OUT_E4M3FN: return down_pick_nb<IN, mxq::kOutE4M3FN>(nb, runs);
+    case MXQ_OUT_E5M2: return down_pick_nb<IN, mxq::kOutE5M2>(nb, runs);
+    default: return down_pick_nb<IN, mxq::kOutE2M1>(nb, runs);
     }
 }
 
 // ---- combine ---------------------------------------------------------------
+
+// Lanes per token: as many as a row has vectors, in steps of 2 from 4 to 64.
+int lanes_for(int64_t vecs)
+{
+    return vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
+}
+
+template <int DT, int WEIGHTED> const void *combine_pick(int lanes)
+{
+    switch (lanes) {
+    case 4: return (const void *)mxq::combine_kernel<DT, WEIGHTED, 4>;
+    case 8: return (const void *)mxq::combine_kernel<DT, WEIGHTED, 8>;
+    case 16: return (const void *)mxq::combine_kernel<DT, WEIGHTED, 16>;
+    case 32: return (const void *)mxq::combine_kernel<DT, WEIGHTED, 32>;
+    default: return (const void *)mxq::combine_kernel<DT, WEIGHTED, 64>;
+    }
+}
 
 template <int DT>
 int combine_launch(const void *y_, int64_t rows, int64_t N, const int32_t *dest, const float *weights, int64_t tokens,
@@ -122,17 +140,31 @@ int combine_launch(const void *y_, int64_t rows, int64_t N, const int32_t *dest,
 {
     typedef typename mxq::Elem<DT>::type T;
     const int64_t vecs = (N + mxq::Elem<DT>::vec - 1) / mxq::Elem<DT>::vec;
-    if (tokens > mxq_host::kMaxWorkItems / vecs - 256)
+    const int lanes = lanes_for(vecs);
+    const int64_t parts = lanes == 64 ? (vecs + 63) / 64 : 1, per = 256 / lanes;
+    if (!grid_fits(tokens, parts, lanes) || !grid_fits((tokens * parts + per - 1) / per, 1, 256))
         return MXQ_E_OVERFLOW;
-    const int64_t blocks = (tokens * vecs + 255) / 256;
-    if (!grid_fits(blocks, 1, 256))
-        return MXQ_E_OVERFLOW;
-    const T *y = (const T *)y_;
     T *out = (T *)out_;
-    uint32_t r = (uint32_t)rows, n = (uint32_t)N, v = (uint32_t)vecs, t = (uint32_t)tokens, s = (uint32_t)slots;
-    const void *k = weights ? (const void *)mxq::combine_kernel<DT, 1> : (const void *)mxq::combine_kernel<DT, 0>;
-    void *args[] = {&y, &r, &n, &v, &dest, &weights, &t, &s, &out};
-    return status_of(hipLaunchKernel(k, dim3((uint32_t)blocks), dim3(256), args, 0, stream));
+    const T *y = rows > 0 ? (const T *)y_ : out;   // row 0 is read (and not used) for a pair without a row
+    uint32_t r = (uint32_t)rows, n = (uint32_t)N, v = (uint32_t)vecs, p = (uint32_t)parts, t = (uint32_t)tokens,
+             s = (uint32_t)slots;
+    const void *k = weights ? combine_pick<DT, 1>(lanes) : combine_pick<DT, 0>(lanes);
+    void *args[] = {&y, &r, &n, &v, &p, &dest, &weights, &t, &s, &out};
+    return status_of(hipLaunchKernel(k, dim3((uint32_t)((tokens * parts + per - 1) / per)), dim3(256), args, 0,
+                                     stream));
+}
+
+template <int DT> const void *combine_backward_pick(int lanes, int64_t vecs)
+{
+    switch (lanes) {
+    case 4: return (const void *)mxq::combine_backward_kernel<DT, 4, 1>;
+    case 8: return (const void *)mxq::combine_backward_kernel<DT, 8, 1>;
+    case 16: return (const void *)mxq::combine_backward_kernel<DT, 16, 1>;
+    case 32: return (const void *)mxq::combine_backward_kernel<DT, 32, 1>;
+    default: break;
+    }
+    return vecs <= 64 ? (const void *)mxq::combine_backward_kernel<DT, 64, 1>
+                      : (const void *)mxq::combine_backward_kernel<DT, 64, 2>;
 }
 
 template <int DT>
@@ -141,20 +173,19 @@ int combine_backward_launch(const void *grad_, const void *y_, int64_t rows, int
                             float *grad_w, hipStream_t stream)
 {
     typedef typename mxq::Elem<DT>::type T;
-    // a wave per token for rows of up to 4 KiB, else a workgroup of 4 waves
-    const bool wide = N * (int64_t)sizeof(T) > 4096;
-    const int64_t per = wide ? 1 : 4;
-    const int64_t token_blocks = (tokens + per - 1) / per, row_blocks = (rows + 255) / 256;
-    if (!grid_fits(token_blocks + row_blocks, 1, 256))
+    const int64_t vecs = (N + mxq::Elem<DT>::vec - 1) / mxq::Elem<DT>::vec;
+    const int lanes = lanes_for(vecs);
+    const int64_t pairs = tokens * slots, per = 256 / lanes;
+    const int64_t row_blocks = (rows + per - 1) / per, pair_blocks = (pairs + 255) / 256;
+    if (!grid_fits(row_blocks + pair_blocks, 1, 256))
         return MXQ_E_OVERFLOW;
     const T *grad = (const T *)grad_, *y = (const T *)y_;
     T *grad_y = (T *)grad_y_;
-    uint32_t r = (uint32_t)rows, n = (uint32_t)N, t = (uint32_t)tokens, s = (uint32_t)slots;
-    uint32_t b = (uint32_t)token_blocks;
-    const void *k = wide ? (const void *)mxq::combine_backward_kernel<DT, 4>
-                         : (const void *)mxq::combine_backward_kernel<DT, 1>;
-    void *args[] = {&grad, &y, &r, &n, &src, &dest, &weights, &t, &s, &b, &grad_y, &grad_w};
-    return status_of(hipLaunchKernel(k, dim3((uint32_t)(token_blocks + row_blocks)), dim3(256), args, 0, stream));
+    uint32_t r = (uint32_t)rows, n = (uint32_t)N, v = (uint32_t)vecs, p = (uint32_t)pairs, s = (uint32_t)slots;
+    uint32_t b = (uint32_t)row_blocks;
+    void *args[] = {&grad, &y, &r, &n, &v, &src, &dest, &weights, &p, &s, &b, &grad_y, &grad_w};
+    return status_of(hipLaunchKernel(combine_backward_pick<DT>(lanes, vecs), dim3((uint32_t)(row_blocks + pair_blocks)),
+                                     dim3(256), args, 0, stream));
 }
 
 int check_elem(int elem_dtype)
@@ -268,7 +299,11 @@ int mxq_moe_gather_quantize(const void *x, int64_t tokens, int64_t slots, int64_
 
     const uint16_t *a0 = (const uint16_t *)x;
     const int32_t *a1 = src;
-    uint32_t a2 = (uint32_t)rows, a3 = (uint32_t)(tokens * slots), a4 = (uint32_t)slots;
+    uint32_t a2 = (uint32_t)rows, a3 = (uint32_t)(tokens * slots);
+    uint32_t shift = 31; // slot_div's constants
+    while ((1ll << (shift - 31)) < slots)
+        shift++;
+    uint32_t mul = (uint32_t)((((uint64_t)1 << shift) + slots - 1) / slots);
     uint64_t a5 = (uint64_t)K;
     int bias = emax_of(out_dtype) - ((flags & MXQ_FLAG_ALT_EMAX) ? 1 : 0);
     uint32_t dense = (flags & MXQ_FLAG_DENSE_SCALE) ? 1u : 0u;
@@ -278,10 +313,13 @@ int mxq_moe_gather_quantize(const void *x, int64_t tokens, int64_t slots, int64_
         const int64_t strips = K / nb, tiles = (strips + 63) / 64;
         if (!grid_fits(rows / 32, tiles, 64))
             return MXQ_E_OVERFLOW;
-        down_fn k = in_dtype == MXQ_IN_BF16 ? down_pick<mxq::kInBF16>(out_dtype, nb)
-                                            : down_pick<mxq::kInF16>(out_dtype, nb);
+        // rows are read again (more than one slot), x does not fit the XCDs'
+        // L2s as it is (4 MiB each), and one run of its columns fits one
+        const bool runs = slots > 1 && tokens * K * 2 > 8 * (4 << 20) && tokens * 512 <= 4 << 20;
+        down_fn k = in_dtype == MXQ_IN_BF16 ? down_pick<mxq::kInBF16>(out_dtype, nb, runs)
+                                            : down_pick<mxq::kInF16>(out_dtype, nb, runs);
         uint32_t a6 = (uint32_t)strips, a7 = (uint32_t)tiles;
-        void *args[] = {&a0, &a1, &a2, &a3, &a4, &a5, &a6, &a7, &bias, &dense, &d, &s};
+        void *args[] = {&a0, &a1, &a2, &a3, &mul, &shift, &a5, &a6, &a7, &bias, &dense, &d, &s};
         return status_of(hipLaunchKernel((const void *)k, dim3((uint32_t)(rows / 32 * tiles)), dim3(64), args, 0,
                                          (hipStream_t)stream));
     }
@@ -290,7 +328,7 @@ int mxq_moe_gather_quantize(const void *x, int64_t tokens, int64_t slots, int64_
         return MXQ_E_OVERFLOW;
     along_fn k = in_dtype == MXQ_IN_BF16 ? along_pick<mxq::kInBF16>(out_dtype) : along_pick<mxq::kInF16>(out_dtype);
     uint32_t a6 = (uint32_t)tiles;
-    void *args[] = {&a0, &a1, &a2, &a3, &a4, &a5, &a6, &bias, &dense, &d, &s};
+    void *args[] = {&a0, &a1, &a2, &a3, &mul, &shift, &a5, &a6, &bias, &dense, &d, &s};
     return status_of(hipLaunchKernel((const void *)k, dim3((uint32_t)(ktiles * tiles)), dim3(64 * mxq::kAlongWaves),
                                      args, 0, (hipStream_t)stream));
 }
