@@ -9,6 +9,7 @@ raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -436,22 +437,28 @@ def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tenso
 
 
 def _check_tensor(name: str, t: torch.Tensor, shape, dtypes, device: torch.device | None = None) -> None:
-    """A contiguous device tensor of this shape (None: any extent) and one of
-    these types, on ``device`` if given."""
+    """A contiguous device tensor of this shape (an int: of that many
+    dimensions) and one of these types, on ``device`` if given."""
+    if t.is_cuda and (device is None or t.device == device) and t.dtype in dtypes and t.is_contiguous() and \
+            (t.dim() == shape if type(shape) is int else t.shape == shape):
+        return
     if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError("%s must be a device tensor%s" % (name, "" if device is None else " on %s" % device))
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError("%s must have shape %s, got %s"
-                         % (name, "[%s]" % ", ".join("*" if n is None else str(n) for n in shape), tuple(t.shape)))
     if t.dtype not in dtypes:
         raise ValueError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must %s, got shape %s" % (
+        name, "have %d dimensions" % shape if type(shape) is int else "have shape %s" % (tuple(shape),),
+        tuple(t.shape)))
 
 
 _INT32 = (torch.int32,)
+_IDS = (torch.int32, torch.int64)
 _FLOAT32 = (torch.float32,)
 _UINT8 = (torch.uint8,)
+_IN = tuple(IN_DTYPES)
+_ELEMS = tuple(ELEM_DTYPES)
 
 
 def _elem_code(dtype: torch.dtype) -> int:
@@ -459,6 +466,20 @@ def _elem_code(dtype: torch.dtype) -> int:
         return ELEM_DTYPES[dtype]
     except KeyError:
         raise MXQError(14, "element type must be bfloat16, float16 or float32, got %s" % dtype) from None
+
+
+@functools.lru_cache(maxsize=256)
+def _sort_sizes(tokens: int, slots: int, experts: int, align: int):
+    """(rows, workspace bytes) of a sort."""
+    return moe_rows(tokens, slots, experts, align), int(load().mxq_moe_sort_workspace_bytes(tokens, slots, experts))
+
+
+@functools.lru_cache(maxsize=256)
+def _gather_sizes(rows: int, K: int, out_dtype: str, dim: int, dense: bool):
+    """(data shape, scale shape, data bytes, scale bytes) of a gathered quantize."""
+    P, F = axis_view_shape(rows, K, dim)
+    return (data_shape(P, F, out_dtype), scale_image_shape(P, F, dense), _data_nbytes(P, F, _out_code(out_dtype)),
+            _scale_nbytes(P, F, FLAG_DENSE_SCALE if dense else 0))
 
 
 def moe_rows(tokens: int, slots: int, experts: int, align: int = 32) -> int:
@@ -482,11 +503,10 @@ def moe_sort(experts: torch.Tensor, num_experts: int, align: int = 32,
     plan has :func:`moe_rows` rows, whatever the assignment.
     """
     lib = load()
-    _check_tensor("experts", experts, (None, None), (torch.int32, torch.int64))
+    _check_tensor("experts", experts, 2, _IDS)
     T, k = experts.shape
     dev = experts.device
-    rows = moe_rows(T, k, num_experts, align)
-    nws = int(lib.mxq_moe_sort_workspace_bytes(T, k, num_experts))
+    rows, nws = _sort_sizes(T, k, num_experts, align)
     offsets = _new((num_experts + 1,), torch.int32, dev, stream)
     src = _new((rows,), torch.int32, dev, stream)
     dest = _new((T, k), torch.int32, dev, stream)
@@ -499,9 +519,10 @@ def moe_sort(experts: torch.Tensor, num_experts: int, align: int = 32,
 
 def _check_plan(plan: MoEPlan, device: torch.device):
     """(rows, tokens, slots) of a plan on ``device``."""
-    _check_tensor("plan.src", plan.src, (None,), _INT32, device)
-    _check_tensor("plan.dest", plan.dest, (None, None), _INT32, device)
-    return (plan.src.shape[0],) + tuple(plan.dest.shape)
+    src, dest = plan.src, plan.dest
+    _check_tensor("plan.src", src, 1, _INT32, device)
+    _check_tensor("plan.dest", dest, 2, _INT32, device)
+    return (*src.shape, *dest.shape)
 
 
 def moe_gather_quantize(x: torch.Tensor, plan: MoEPlan, out_dtype: str = "e4m3fn", dim: int = -1,
@@ -521,22 +542,24 @@ def moe_gather_quantize(x: torch.Tensor, plan: MoEPlan, out_dtype: str = "e4m3fn
     code = _out_code(out_dtype)
     if x.dtype not in IN_DTYPES:
         raise MXQError(1, "input must be bfloat16 or float16, got %s" % x.dtype)
-    _check_tensor("x", x, (None, None), tuple(IN_DTYPES))
-    rows, T, k = _check_plan(plan, x.device)
-    K = x.shape[1]
-    if x.shape[0] != T:
-        raise ValueError("x has %d rows, the plan %d tokens" % (x.shape[0], T))
-    P, F = axis_view_shape(rows, K, dim)
+    _check_tensor("x", x, 2, _IN)
+    dev = x.device
+    rows, T, k = _check_plan(plan, dev)
+    n, K = x.shape
+    if n != T:
+        raise ValueError("x has %d rows, the plan %d tokens" % (n, T))
+    dshape, sshape, dbytes, sbytes = _gather_sizes(rows, K, out_dtype, dim, dense_scale)
     flags = (FLAG_ALT_EMAX if alt_emax else 0) | (FLAG_DENSE_SCALE if dense_scale else 0)
     if data_out is None:
-        data_out = _new(data_shape(P, F, out_dtype), torch.uint8, x.device, stream)
+        data_out = _new(dshape, torch.uint8, dev, stream)
+    else:
+        _check_out_buffer("data_out", data_out, dbytes, dev)
     if scale_out is None:
-        scale_out = _new(scale_image_shape(P, F, dense_scale), torch.uint8, x.device, stream)
-    _check_out_buffer("data_out", data_out, _data_nbytes(P, F, code), x.device)
-    _check_out_buffer("scale_out", scale_out, _scale_nbytes(P, F, flags), x.device)
-    _check(_call_on(x.device, lib.mxq_moe_gather_quantize, x.data_ptr(), T, k, K, IN_DTYPES[x.dtype], code, dim, flags,
-                    plan.src.data_ptr(), rows, data_out.data_ptr(), scale_out.data_ptr(),
-                    _stream_handle(stream, x.device)))
+        scale_out = _new(sshape, torch.uint8, dev, stream)
+    else:
+        _check_out_buffer("scale_out", scale_out, sbytes, dev)
+    _check(_call_on(dev, lib.mxq_moe_gather_quantize, x.data_ptr(), T, k, K, IN_DTYPES[x.dtype], code, dim, flags,
+                    plan.src.data_ptr(), rows, data_out.data_ptr(), scale_out.data_ptr(), _stream_handle(stream, dev)))
     return data_out, scale_out
 
 
@@ -551,20 +574,21 @@ def moe_combine(y: torch.Tensor, plan: MoEPlan, weights: torch.Tensor | None = N
     """
     lib = load()
     code = _elem_code(y.dtype)
-    _check_tensor("y", y, (None, None), tuple(ELEM_DTYPES))
-    rows, T, k = _check_plan(plan, y.device)
-    if y.shape[0] != rows:
-        raise ValueError("y has %d rows, the plan %d" % (y.shape[0], rows))
-    N = y.shape[1]
+    _check_tensor("y", y, 2, _ELEMS)
+    dev = y.device
+    rows, T, k = _check_plan(plan, dev)
+    n, N = y.shape
+    if n != rows:
+        raise ValueError("y has %d rows, the plan %d" % (n, rows))
     if weights is not None:
-        _check_tensor("weights", weights, (T, k), _FLOAT32, y.device)
+        _check_tensor("weights", weights, (T, k), _FLOAT32, dev)
     if out is None:
-        out = _new((T, N), y.dtype, y.device, stream)
+        out = _new((T, N), y.dtype, dev, stream)
     else:
-        _check_tensor("out", out, (T, N), (y.dtype,), y.device)
-    _check(_call_on(y.device, lib.mxq_moe_combine, y.data_ptr(), rows, N, code, plan.dest.data_ptr(),
+        _check_tensor("out", out, (T, N), (y.dtype,), dev)
+    _check(_call_on(dev, lib.mxq_moe_combine, y.data_ptr(), rows, N, code, plan.dest.data_ptr(),
                     None if weights is None else weights.data_ptr(), T, k, out.data_ptr(),
-                    _stream_handle(stream, y.device)))
+                    _stream_handle(stream, dev)))
     return out
 
 
@@ -580,24 +604,25 @@ def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, plan: MoEPlan, wei
     """
     lib = load()
     code = _elem_code(y.dtype)
-    _check_tensor("y", y, (None, None), tuple(ELEM_DTYPES))
-    rows, T, k = _check_plan(plan, y.device)
-    if y.shape[0] != rows:
-        raise ValueError("y has %d rows, the plan %d" % (y.shape[0], rows))
-    N = y.shape[1]
-    _check_tensor("grad", grad, (T, N), (y.dtype,), y.device)
-    _check_tensor("weights", weights, (T, k), _FLOAT32, y.device)
+    _check_tensor("y", y, 2, _ELEMS)
+    dev = y.device
+    rows, T, k = _check_plan(plan, dev)
+    n, N = y.shape
+    if n != rows:
+        raise ValueError("y has %d rows, the plan %d" % (n, rows))
+    _check_tensor("grad", grad, (T, N), (y.dtype,), dev)
+    _check_tensor("weights", weights, (T, k), _FLOAT32, dev)
     if grad_y is None:
-        grad_y = _new((rows, N), y.dtype, y.device, stream)
+        grad_y = _new((rows, N), y.dtype, dev, stream)
     else:
-        _check_tensor("grad_y", grad_y, (rows, N), (y.dtype,), y.device)
+        _check_tensor("grad_y", grad_y, (rows, N), (y.dtype,), dev)
     if grad_weights is None:
-        grad_weights = _new((T, k), torch.float32, y.device, stream)
+        grad_weights = _new((T, k), torch.float32, dev, stream)
     else:
-        _check_tensor("grad_weights", grad_weights, (T, k), _FLOAT32, y.device)
-    _check(_call_on(y.device, lib.mxq_moe_combine_backward, grad.data_ptr(), y.data_ptr(), rows, N, code,
+        _check_tensor("grad_weights", grad_weights, (T, k), _FLOAT32, dev)
+    _check(_call_on(dev, lib.mxq_moe_combine_backward, grad.data_ptr(), y.data_ptr(), rows, N, code,
                     plan.src.data_ptr(), plan.dest.data_ptr(), weights.data_ptr(), T, k, grad_y.data_ptr(),
-                    grad_weights.data_ptr(), _stream_handle(stream, y.device)))
+                    grad_weights.data_ptr(), _stream_handle(stream, dev)))
     return grad_y, grad_weights
 
 
@@ -620,13 +645,14 @@ def grouped_scaled_matmul(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs: torch
     code = _out_code(fmt)
     if res_dtype not in RES_DTYPES:
         raise MXQError(10, "result type must be float32 or bfloat16, got %s" % res_dtype)
-    _check_tensor("lhs", lhs, (None, None), _UINT8)
+    _check_tensor("lhs", lhs, 2, _UINT8)
     dev = lhs.device
-    P, M = lhs.shape[0], lhs.shape[1] // 4
-    _check_tensor("rhs", rhs, (None, P, None), _UINT8, dev)
-    G, N = rhs.shape[0], rhs.shape[2] // 4
-    if lhs.shape[1] % 4 or rhs.shape[2] % 4 or P % 8:
-        raise ValueError("lhs [P, 4 rows] and rhs [groups, P, 4 N] need P % 8 == 0")
+    _check_tensor("rhs", rhs, 3, _UINT8, dev)
+    P, M4 = lhs.shape
+    G, P2, N4 = rhs.shape
+    if P2 != P or M4 % 4 or N4 % 4 or P % 8:
+        raise ValueError("lhs [P, 4 rows] and rhs [groups, P, 4 N] must share P, a multiple of 8")
+    M, N = M4 // 4, N4 // 4
     _check_tensor("lhs_scale", lhs_scale, (P // 8, M), _UINT8, dev)
     _check_tensor("rhs_scale", rhs_scale, (G, P // 8, N), _UINT8, dev)
     _check_tensor("offsets", offsets, (G + 1,), _INT32, dev)
@@ -658,7 +684,7 @@ def grouped_scaled_matmul_wgrad(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs:
         raise MXQError(10, "result type must be float32 or bfloat16, got %s" % res_dtype)
     P, M, N = _check_operands(lhs, lhs_scale, rhs, rhs_scale, True)
     dev = lhs.device
-    _check_tensor("offsets", offsets, (None,), _INT32, dev)
+    _check_tensor("offsets", offsets, 1, _INT32, dev)
     G = offsets.shape[0] - 1
     if out is None:
         out = _new((max(G, 0), M, N), res_dtype, dev, stream)
@@ -674,34 +700,55 @@ def grouped_scaled_matmul_wgrad(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs:
 # Gradient norm and clipping
 # ---------------------------------------------------------------------------
 
+def _check_tensors(name, tensors, device):
+    """Contiguous device tensors of element types, as (addresses, elements,
+    type codes). A list may hold hundreds: one pass per property, each at the
+    interpreter's C speed."""
+    T = torch.Tensor
+    codes = [ELEM_DTYPES.get(t.dtype) for t in tensors]
+    if None in codes or not all(map(T.is_contiguous, tensors)) or {t.device for t in tensors} != {device}:
+        for t in tensors:
+            _check_tensor(name, t, t.dim(), _ELEMS, device)
+    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), codes
+
+
+def _c_array(typecode: str, values):
+    a = array.array(typecode, values)
+    return a, a.buffer_info()[0]    # (the array keeps the memory)
+
+
 def _norm_call(grads, max_norm, outs, stream):
     lib = load()
-    grads = list(grads)
     if not grads:
         raise ValueError("no tensors")
     dev = grads[0].device
-    for name, ts in (("grads", grads), ("out", outs or ())):
-        for t in ts:
-            _check_tensor(name, t, (None,) * t.dim(), tuple(ELEM_DTYPES), dev)
-    if outs is not None and (len(outs) != len(grads) or
-                             any(o.dtype != g.dtype or o.shape != g.shape for o, g in zip(outs, grads))):
-        raise ValueError("out must hold a tensor of each gradient's shape and type")
+    if dev.type != "cuda":
+        raise ValueError("grads must be device tensors")
+    ptrs, numels, codes = _check_tensors("grads", grads, dev)
+    if outs is None:
+        optrs = None
+    elif outs is grads:
+        optrs = ptrs
+    else:
+        optrs, _, ocodes = _check_tensors("out", outs, dev)
+        if ocodes != codes or [o.shape for o in outs] != [g.shape for g in grads]:
+            raise ValueError("out must hold a tensor of each gradient's shape and type")
     n = len(grads)
-    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
-    optrs = None if outs is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
-    numels = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    codes = (ctypes.c_int * n)(*[ELEM_DTYPES[g.dtype] for g in grads])
+    pa, pp = _c_array("Q", ptrs)
+    oa, op = (None, None) if optrs is None else (pa, pp) if optrs is ptrs else _c_array("Q", optrs)
+    na, np_ = _c_array("q", numels)
+    ca, cp = _c_array("i", codes)
     norm = _new((), torch.float32, dev, stream)
-    ws = _new((int(lib.mxq_clip_grad_norm_workspace_bytes(numels, codes, n)),), torch.uint8, dev, stream)
-    _check(_call_on(dev, lib.mxq_clip_grad_norm, ptrs, optrs, numels, codes, n, max_norm, norm.data_ptr(),
-                    ws.data_ptr(), _stream_handle(stream, dev)))
+    ws = _new((lib.mxq_clip_grad_norm_workspace_bytes(np_, cp, n),), torch.uint8, dev, stream)
+    _check(_call_on(dev, lib.mxq_clip_grad_norm, pp, op, np_, cp, n, max_norm, norm.data_ptr(), ws.data_ptr(),
+                    _stream_handle(stream, dev)))
     return norm
 
 
 def grad_norm(grads, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """The norm of all elements of all tensors (bf16, f16 or f32, mixed), as a
     float32 device scalar; the squares are added in 64 bits."""
-    return _norm_call(grads, 0.0, None, stream)
+    return _norm_call(list(grads), 0.0, None, stream)
 
 
 def clip_grad_norm(grads, max_norm: float, out=None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:

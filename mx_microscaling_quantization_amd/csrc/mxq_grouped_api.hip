@@ -8,6 +8,22 @@
 #include "mxq_host.hpp"
 #include "mxq_grouped_kernels.hpp"
 
+#ifndef M1
+#define M1 96
+#endif
+#ifndef M2
+#define M2 96
+#endif
+#ifndef XCW
+#define XCW 2
+#define XKW 2
+#endif
+#ifndef SD1
+#define SD1 2
+#endif
+#ifndef SD2
+#define SD2 2
+#endif
 namespace {
 
 using mxq_host::grid_fits;
@@ -20,8 +36,8 @@ template <int FMT, int EPI> grouped_fn pick_kernel(int kind)
     switch (kind) {
     case 0: return mxq::grouped_matmul_kernel<FMT, EPI, mxq::kGroupRows>;
     case 1: return mxq::grouped_matmul_kernel<FMT, EPI, mxq::kGroupWgrad>;
-    case 2: return mxq::grouped_stream_kernel<FMT, EPI, 1, 4>;
-    default: return mxq::grouped_stream_kernel<FMT, EPI, 2, 4>;
+    case 2: return mxq::grouped_stream_kernel<FMT, EPI, 1, XCW, XKW, SD1>;
+    default: return mxq::grouped_stream_kernel<FMT, EPI, 2, 1, 4, SD2>;
     }
 }
 
@@ -89,10 +105,10 @@ int mxq_grouped_matmul(const void *lhs, const void *lhs_scale, const void *rhs, 
     // the last one) may end with a part of a tile. The tile follows from the
     // mean rows per group.
     const int64_t mean = rows / groups;
-    const int kind = mean <= 48 ? 2 : mean <= 96 ? 3 : 0;
+    const int kind = mean <= M1 ? 2 : mean <= M2 ? 3 : 0;
     const int64_t tile = kind == 2 ? 32 : kind == 3 ? 64 : mxq::kMmTile;
-    const int64_t cols = kind ? mxq::kStreamCols : mxq::kMmTile;
-    const uint32_t threads = kind ? 256 : mxq::kMmThreads;
+    const int64_t cols = kind == 2 ? XCW * mxq::kStreamCols : kind ? mxq::kStreamCols : mxq::kMmTile;
+    const uint32_t threads = kind ? kind == 2 ? 64 * XCW * XKW : 256 : mxq::kMmThreads;
     const int64_t tiles_m = rows / tile + groups + 1, tiles_n = (N + cols - 1) / cols;
     if (!grid_fits(tiles_m, tiles_n, threads))
         return MXQ_E_OVERFLOW;

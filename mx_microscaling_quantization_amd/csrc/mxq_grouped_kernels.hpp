@@ -113,6 +113,34 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t w, uint32_t n)
 }
 
 // ----------------------------------------------------------------------------
+// Results
+// ----------------------------------------------------------------------------
+
+// Two fp32 values as bf16 bits, rounded to nearest even by the conversion
+// instruction (the scaled matmul's own six-instruction rounding, one value at a
+// time, took 2 us of a 256 x 256 tile).
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b)
+{
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, bf16x2_t));
+}
+
+// 4 adjacent results of row m from column col on; N % 4 == 0.
+template <int EPI>
+__device__ __forceinline__ void grouped_store(const float *v, uint32_t m, uint32_t row_end, uint32_t col, uint32_t N,
+                                              void *__restrict__ out)
+{
+    if (m >= row_end || col >= N)
+        return;
+    const uint64_t o = (uint64_t)m * N + col;
+    if constexpr (EPI == kEpiF32)
+        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + o) = float4{v[0], v[1], v[2], v[3]};
+    else
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(out) + o) =
+            uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+}
+
+// ----------------------------------------------------------------------------
 // Many rows per group: the scaled matmul's 256 x 256 tile
 // ----------------------------------------------------------------------------
 
@@ -200,7 +228,14 @@ __global__ __launch_bounds__(kMmThreads) void grouped_matmul_kernel(
         mm_rare_part<F, EPI>(lhs, lhs_scale, rhs, rhs_scale, P, M, N, wm0, wn0, 1u, out, nullptr, 0, row_end);
         __builtin_amdgcn_endpgm();
     }
-    mm_epilogue<EPI>(acc, wm0, wn0, row_end, N, out, nullptr, 0, 1u, lane & 31u, lane >> 5);
+    const uint32_t i = lane & 31u, h = lane >> 5;
+#pragma unroll
+    for (int r = 0; r < 16; r++)
+#pragma unroll
+        for (int a = 0; a < 2; a++) {
+            const float v[4] = {acc[a][0][r], acc[a][1][r], acc[a][2][r], acc[a][3][r]};
+            grouped_store<EPI>(v, wm0 + 16u * (r >> 2) + 8u * h + 2u * (r & 3) + a, row_end, wn0 + 4u * i, N, out);
+        }
 }
 
 // ----------------------------------------------------------------------------
@@ -211,7 +246,7 @@ __global__ __launch_bounds__(kMmThreads) void grouped_matmul_kernel(
 // workgroup of WAVES waves computes 32 * MS rows x 128 columns; each wave takes
 // its share of the K steps, loads the weights straight into the MFMA's lane
 // mapping (16 bytes per lane and operand row: 512 contiguous bytes of each
-// row) with the next step's loads in flight, and keeps its own sums. At the
+// row) with the next steps' loads in flight, and keeps its own sums. At the
 // end the waves' sums are added through LDS, in wave order, one 32-row
 // sub-tile at a time.
 //
@@ -227,11 +262,21 @@ template <int MS> struct StreamRaw {
     uint32_t as, bs;     // byte a (u): the scale of A sub-tile a (B sub-tile u)
 };
 
+// The operand bytes and scales of K step `step`, or zeros without any access to
+// memory where step >= end (end <= the number of steps).
 template <int MS>
 __device__ __forceinline__ void stream_load(StreamRaw<MS> &r, const MmSource &sa, const MmSource &sb, uint32_t P,
-                                            uint32_t step, uint32_t i, uint32_t h)
+                                            uint32_t step, uint32_t end, uint32_t i, uint32_t h)
 {
-    const __amdgpu_buffer_rsrc_t ra = mm_step_rsrc(sa, P, step), rb = mm_step_rsrc(sb, P, step);
+    const bool in = step < end;
+    step = in ? step : 0u;
+    const uint32_t nrows = in ? min(P - step * kMmStepRows, kMmStepRows) : 0u;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(sa.data + (uint64_t)step * kMmStepRows * sa.pitch), (short)0,
+        in ? (int)(nrows * sa.pitch - sa.col_bytes) : 0, kMmBufferFlags);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(sb.data + (uint64_t)step * kMmStepRows * sb.pitch), (short)0,
+        in ? (int)(nrows * sb.pitch - sb.col_bytes) : 0, kMmBufferFlags);
     const uint32_t va = 4u * h * sa.pitch + 4u * MS * i, vb = 4u * h * sb.pitch + 16u * i;
 #pragma unroll
     for (int v = 0; v < 8; v++) {
@@ -255,11 +300,13 @@ __device__ __forceinline__ void stream_load(StreamRaw<MS> &r, const MmSource &sa
         }
     }
     // the step's scale rows 2 step + h, from the tile's first column on
-    const uint32_t blocks = min(P / 8u - 2u * step, 2u);
+    const uint32_t blocks = nrows / 8u;
     const __amdgpu_buffer_rsrc_t qa = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(sa.scale + 2ull * step * sa.C), (short)0, (int)(blocks * sa.C - sa.col_bytes / 4u), kMmBufferFlags);
+        (void *)(sa.scale + 2ull * step * sa.C), (short)0, in ? (int)(blocks * sa.C - sa.col_bytes / 4u) : 0,
+        kMmBufferFlags);
     const __amdgpu_buffer_rsrc_t qb = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(sb.scale + 2ull * step * sb.C), (short)0, (int)(blocks * sb.C - sb.col_bytes / 4u), kMmBufferFlags);
+        (void *)(sb.scale + 2ull * step * sb.C), (short)0, in ? (int)(blocks * sb.C - sb.col_bytes / 4u) : 0,
+        kMmBufferFlags);
     if constexpr (MS == 1)
         r.as = __builtin_amdgcn_raw_buffer_load_b8(qa, h * sa.C + i, 0, 0);
     else if constexpr (MS == 2)
@@ -289,21 +336,6 @@ __device__ __forceinline__ void stream_products(f32x16_t (&acc)[MS][4], const St
     }
 }
 
-// One row's 4 adjacent results.
-template <int EPI>
-__device__ __forceinline__ void stream_store(const float *v, uint32_t m, uint32_t row_end, uint32_t col, uint32_t N,
-                                             void *__restrict__ out)
-{
-    if (m >= row_end || col >= N)
-        return;
-    const uint64_t o = (uint64_t)m * N + col;
-    if constexpr (EPI == kEpiF32)
-        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + o) = float4{v[0], v[1], v[2], v[3]};
-    else
-        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(out) + o) =
-            uint2{mm_bf16_bits(v[0]) | mm_bf16_bits(v[1]) << 16, mm_bf16_bits(v[2]) | mm_bf16_bits(v[3]) << 16};
-}
-
 // The rare path (scale bytes of 255, see mm_step_255): one wave computes
 // sub-tile `a` over all K steps and stores it.
 template <int F, int EPI, int MS>
@@ -324,7 +356,7 @@ __device__ __attribute__((noinline)) void stream_rare_part(const uint8_t *lhs, c
     const uint32_t nsteps = (P + kMmStepRows - 1) / kMmStepRows;
     for (uint32_t s = 0; s < nsteps; s++) {
         StreamRaw<MS> r;
-        stream_load<MS>(r, sa, sb, P, s, i, h);
+        stream_load<MS>(r, sa, sb, P, s, nsteps, i, h);
         i32x8_t av, bv[4];
 #pragma unroll
         for (int v = 0; v < 8; v++) {
@@ -344,22 +376,23 @@ __device__ __attribute__((noinline)) void stream_rare_part(const uint8_t *lhs, c
 #pragma unroll
     for (int r = 0; r < 16; r++) {
         const float v[4] = {acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
-        stream_store<EPI>(v, m0 + MS * (8u * (r >> 2) + 4u * h + (r & 3)) + a, row_end, n0 + 4u * i, N, out);
+        grouped_store<EPI>(v, m0 + MS * (8u * (r >> 2) + 4u * h + (r & 3)) + a, row_end, n0 + 4u * i, N, out);
     }
 }
 
-template <int FMT, int EPI, int MS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(
+template <int FMT, int EPI, int MS, int CW, int KW, int DEPTH>
+__global__ __launch_bounds__(64 * CW * KW, 2) void grouped_stream_kernel(
     const uint8_t *__restrict__ lhs, const uint8_t *__restrict__ lhs_scale, const uint8_t *__restrict__ rhs,
     const uint8_t *__restrict__ rhs_scale, const int32_t *__restrict__ offsets, uint32_t groups, uint32_t P,
     uint32_t M, uint32_t N, uint32_t tiles_n, void *__restrict__ out)
 {
     constexpr int F = MfmaFmt<FMT>::value;
-    constexpr uint32_t TILE = 32 * MS, RW = 16 / WAVES;   // result registers each wave adds up
-    __shared__ __attribute__((aligned(16))) float sums[WAVES][16][64][4];
-    __shared__ uint32_t rare[MS];
+    constexpr uint32_t TILE = 32 * MS, RW = 16 / KW;   // result registers each wave adds up
+    __shared__ __attribute__((aligned(16))) float sums[CW][KW][16][64][4];
+    __shared__ uint32_t rare[MS][CW];
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t cw = wave % CW, kw = wave / CW;
     const uint32_t i = lane & 31u, h = lane >> 5;
 
     const GroupScan sc = group_scan<TILE>(offsets, groups, M, lane);
@@ -368,7 +401,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(
         return;
     const uint32_t tr = t / tiles_n;
     const GroupTile g = group_find<TILE>(offsets, groups, M, sc, tr);
-    const uint32_t n0 = (t - tr * tiles_n) * kStreamCols;
+    const uint32_t n0 = ((t - tr * tiles_n) * CW + cw) * kStreamCols;
     if (g.group >= groups) {
         P = 0;
     } else {
@@ -378,8 +411,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(
     MmSource sa, sb;
     mm_source(sa, lhs, lhs_scale, M, g.m0);
     mm_source(sb, rhs, rhs_scale, N, n0);
-    if (threadIdx.x < MS)
-        rare[threadIdx.x] = 0;
+    if (threadIdx.x < MS * CW)
+        (&rare[0][0])[threadIdx.x] = 0;
 
     f32x16_t acc[MS][4];
 #pragma unroll
@@ -387,21 +420,23 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(
 #pragma unroll
         for (int u = 0; u < 4; u++)
             acc[a][u] = f32x16_t{};
-    const uint32_t nsteps = (P + kMmStepRows - 1) / kMmStepRows;
-    const uint32_t per = (nsteps + WAVES - 1) / WAVES;
-    const uint32_t s0 = min(wave * per, nsteps), s1 = min(s0 + per, nsteps);
-    // two register sets: one step's loads are in flight while the other's
-    // products are taken (a step past the last loads that one again)
-    if (s0 < s1) {
-        StreamRaw<MS> r0, r1;
-        stream_load<MS>(r0, sa, sb, P, s0, i, h);
-        for (uint32_t s = s0; s < s1; s += 2) {
-            stream_load<MS>(r1, sa, sb, P, min(s + 1u, s1 - 1u), i, h);
-            stream_products<F, MS>(acc, r0);
-            if (s + 1 >= s1)
-                break;
-            stream_load<MS>(r0, sa, sb, P, min(s + 2u, s1 - 1u), i, h);
-            stream_products<F, MS>(acc, r1);
+    const uint32_t nsteps = n0 < N ? (P + kMmStepRows - 1) / kMmStepRows : 0u;
+    const uint32_t per = (nsteps + KW - 1) / KW;
+    const uint32_t s0 = min(kw * per, nsteps), s1 = min(s0 + per, nsteps);
+    // DEPTH register sets: the loads of DEPTH - 1 steps are in flight while one
+    // step's products are taken. (Without the scheduling fences the compiler
+    // moves the loads behind the products, and nothing overlaps.)
+    StreamRaw<MS> raw[DEPTH];
+#pragma unroll
+    for (uint32_t d = 0; d < DEPTH - 1; d++)
+        stream_load<MS>(raw[d], sa, sb, P, s0 + d, s1, i, h);
+    for (uint32_t s = s0; s < s1; s += DEPTH) {
+#pragma unroll
+        for (uint32_t d = 0; d < DEPTH; d++) {
+            stream_load<MS>(raw[(d + DEPTH - 1) % DEPTH], sa, sb, P, s + d + DEPTH - 1, s1, i, h);
+            __builtin_amdgcn_sched_barrier(0);
+            stream_products<F, MS>(acc, raw[d]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 
@@ -409,18 +444,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(
     for (int a = 0; a < MS; a++) {
 #pragma unroll
         for (int r = 0; r < 16; r++)
-            *reinterpret_cast<float4 *>(sums[wave][r][lane]) =
+            *reinterpret_cast<float4 *>(sums[cw][kw][r][lane]) =
                 float4{acc[a][0][r], acc[a][1][r], acc[a][2][r], acc[a][3][r]};
         __syncthreads();
         float v[RW][4];
         bool finite = true;
 #pragma unroll
         for (uint32_t k = 0; k < RW; k++) {
-            const uint32_t r = wave * RW + k;
-            float4 x = *reinterpret_cast<const float4 *>(sums[0][r][lane]);
+            const uint32_t r = kw * RW + k;
+            float4 x = *reinterpret_cast<const float4 *>(sums[cw][0][r][lane]);
 #pragma unroll
-            for (int w = 1; w < WAVES; w++) {
-                const float4 y = *reinterpret_cast<const float4 *>(sums[w][r][lane]);
+            for (int w = 1; w < KW; w++) {
+                const float4 y = *reinterpret_cast<const float4 *>(sums[cw][w][r][lane]);
                 x.x += y.x;
                 x.y += y.y;
                 x.z += y.z;
@@ -434,18 +469,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(
                      __builtin_isfinite(x.w);
         }
         if (__builtin_amdgcn_ballot_w64(!finite) != 0 && lane == 0)
-            atomicOr(&rare[a], 1u);
+            atomicOr(&rare[a][cw], 1u);
         __syncthreads();   // and every wave has read this sub-tile's sums
-        if (rare[a]) {
-            if (wave == 0)
+        if (rare[a][cw]) {
+            if (kw == 0)
                 stream_rare_part<F, EPI, MS>(lhs, lhs_scale, rhs, rhs_scale, P, M, N, g.m0, n0, g.end, (uint32_t)a,
                                              out);
             continue;
         }
 #pragma unroll
         for (uint32_t k = 0; k < RW; k++) {
-            const uint32_t r = wave * RW + k;
-            stream_store<EPI>(v[k], g.m0 + MS * (8u * (r >> 2) + 4u * h + (r & 3u)) + a, g.end, n0 + 4u * i, N, out);
+            const uint32_t r = kw * RW + k;
+            grouped_store<EPI>(v[k], g.m0 + MS * (8u * (r >> 2) + 4u * h + (r & 3u)) + a, g.end, n0 + 4u * i, N, out);
         }
     }
 }
