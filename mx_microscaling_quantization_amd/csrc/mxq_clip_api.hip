@@ -9,8 +9,13 @@
 
 namespace {
 
-// Workgroups of a launch: 8 per CU, fewer when there are not that many tiles.
+// Workgroups of a norm launch: 8 per CU, fewer when there are not that many tiles.
 constexpr uint32_t kClipBlocks = 2048;
+
+// Elements of a tensor and tiles of a launch, for a dispatch's 2^32 work-items:
+// one tensor has at most 2^36 * 4 bytes in tiles of 2^15.
+constexpr int64_t kMaxElements = (int64_t)1 << 36;
+constexpr uint64_t kMaxTiles = (uint64_t)1 << 23;
 
 uint32_t elem_bytes(int type) { return type == MXQ_ELEM_F32 ? 4u : 2u; }
 
@@ -31,14 +36,14 @@ int check_tensors(const int64_t *elements, const int *types, int64_t count)
             return MXQ_E_ELEM_DTYPE;
         if (elements[i] < 0)
             return MXQ_E_ROWS;
-        if (elements[i] > (int64_t)1 << 40)
+        if (elements[i] > kMaxElements)
             return MXQ_E_OVERFLOW;
     }
     return MXQ_OK;
 }
 
 // The next launch's table from tensor `*next` on: up to kClipTensors tensors
-// that have elements, and at most 2^31 tiles. Returns its workgroups.
+// that have elements, and at most kMaxTiles. Returns its workgroups.
 uint32_t fill(mxq::ClipTable &t, const void *const *in, void *const *out, const int64_t *elements, const int *types,
               int64_t count, int64_t *next)
 {
@@ -50,8 +55,8 @@ uint32_t fill(mxq::ClipTable &t, const void *const *in, void *const *out, const 
         if (elements[i] == 0)
             continue;
         const uint64_t more = tiles_of(elements[i], types[i]);
-        if (tiles + more > (uint64_t)1 << 31)
-            break;   // (one tensor alone has at most 2^28 tiles)
+        if (tiles + more > kMaxTiles)
+            break;
         tiles += more;
         t.in[t.tensors] = in ? in[i] : nullptr;
         t.out[t.tensors] = out ? out[i] : nullptr;
@@ -109,7 +114,7 @@ int mxq_clip_grad_norm(const void *const *grads, void *const *outs, const int64_
 
     mxq::ClipTable t;
     double *partial = (double *)workspace;
-    uint32_t total = 0;
+    uint32_t total = 0, most = 0;   // partial sums; tiles of the largest launch
     int launches = 0;
     hipError_t err = hipSuccess;
     for (int64_t next = 0; next < count && err == hipSuccess;) {
@@ -121,11 +126,14 @@ int mxq_clip_grad_norm(const void *const *grads, void *const *outs, const int64_
         err = hipLaunchKernel((const void *)mxq::clip_norm_kernel, dim3(blocks), dim3(mxq::kClipThreads), args, 0,
                               (hipStream_t)stream);
         total += blocks;
+        most = t.first_tile[t.tensors] > most ? t.first_tile[t.tensors] : most;
         launches++;
     }
-    // One launch's partial sums are added by the scaling pass itself; of
-    // several, or where nothing is scaled, by a launch of its own.
-    const bool own_total = !outs || launches != 1;
+    // One launch's partial sums are added by the scaling pass itself, every
+    // workgroup reading all of them; of several, or where there are many
+    // tiles (a workgroup for each then), or where nothing is scaled, by a
+    // launch of its own.
+    const bool own_total = !outs || launches != 1 || most > 2 * kClipBlocks;
     if (own_total && err == hipSuccess) {
         void *args[] = {&partial, &total, &norm};
         err = hipLaunchKernel((const void *)mxq::clip_total_kernel, dim3(1), dim3(mxq::kClipThreads), args, 0,
@@ -141,8 +149,9 @@ int mxq_clip_grad_norm(const void *const *grads, void *const *outs, const int64_
         if (blocks == 0)
             continue;
         void *args[] = {&t, &sums, &n, &max_norm, &place, &norm_out};
-        err = hipLaunchKernel((const void *)mxq::clip_scale_kernel, dim3(blocks), dim3(mxq::kClipThreads), args, 0,
-                              (hipStream_t)stream);
+        const uint32_t tiles = t.first_tile[t.tensors];
+        err = hipLaunchKernel((const void *)mxq::clip_scale_kernel, dim3(own_total ? tiles : blocks),
+                              dim3(mxq::kClipThreads), args, 0, (hipStream_t)stream);
     }
     return err == hipSuccess ? MXQ_OK : MXQ_E_HIP;
 }

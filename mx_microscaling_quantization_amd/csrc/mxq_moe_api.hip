@@ -42,15 +42,21 @@ int status_of(hipError_t err) { return err == hipSuccess ? MXQ_OK : MXQ_E_HIP; }
 
 // ---- sort ------------------------------------------------------------------
 
-// One workgroup up to this many pairs.
-constexpr int64_t kSortOneBlock = 8192;
-constexpr int64_t kSortChunk = 4096;   // pairs per workgroup until there are kSortBlocks of them
+// One workgroup up to this many pairs (4096 pairs: 7.9 us; 8192: 12.2 us in
+// one workgroup, 8.7 in two launches).
+constexpr int64_t kSortOneBlock = 4096;
 
-int64_t sort_blocks(int64_t pairs)
+// Workgroups of a longer list: 2048 pairs each, 4096 where every workgroup's
+// reading all chunks' counts would be the larger part (524288 pairs and 256
+// experts: 17.3 us with 2048, 14.9 with 4096; with 8 experts 10.4 and 11.0),
+// and more where that makes more than kSortBlocks.
+int64_t sort_blocks(int64_t pairs, int64_t experts)
 {
     if (pairs <= kSortOneBlock)
         return 1;
-    const int64_t b = (pairs + kSortChunk - 1) / kSortChunk;
+    int64_t b = (pairs + 2047) / 2048;
+    if (b * b * experts * 4 > 32 << 20)
+        b = (pairs + 4095) / 4096;
     return b < mxq::kSortBlocks ? b : mxq::kSortBlocks;
 }
 
@@ -58,26 +64,26 @@ template <typename ID>
 int sort_launch(const void *ids_, int64_t pairs, int64_t experts, int64_t align, int64_t rows, int32_t *offsets,
                 int32_t *src, int32_t *dest, void *workspace, hipStream_t stream)
 {
-    const int64_t blocks = sort_blocks(pairs);
+    const int64_t blocks = sort_blocks(pairs, experts);
     const int64_t step = mxq::kSortThreads;   // 64 pairs per wave
     const ID *ids = (const ID *)ids_;
     uint32_t n = (uint32_t)pairs, chunk = (uint32_t)((pairs + blocks * step - 1) / (blocks * step) * step);
-    uint32_t e = (uint32_t)experts, a = (uint32_t)align, r = (uint32_t)rows, bits = 0;
+    uint32_t e = (uint32_t)experts, pitch = (e + 3u) & ~3u, a = (uint32_t)align, r = (uint32_t)rows, bits = 0;
     while ((1u << bits) < e)
         bits++;
     uint32_t *counts = (uint32_t *)workspace;
     if (blocks > 1) {
-        void *args[] = {&ids, &n, &chunk, &e, &counts};
+        void *args[] = {&ids, &n, &chunk, &e, &pitch, &counts};
         const hipError_t err = hipLaunchKernel((const void *)mxq::sort_count_kernel<ID>, dim3((uint32_t)blocks),
-                                               dim3(mxq::kSortThreads), args, 4 * e, stream);
+                                               dim3(mxq::kSortThreads), args, 4 * pitch, stream);
         if (err != hipSuccess)
             return MXQ_E_HIP;
     }
     const void *k = blocks > 1 ? (const void *)mxq::sort_place_kernel<ID, 0>
                                : (const void *)mxq::sort_place_kernel<ID, 1>;
-    void *args[] = {&ids, &n, &chunk, &e, &a, &r, &bits, &counts, &offsets, &src, &dest};
+    void *args[] = {&ids, &n, &chunk, &e, &pitch, &a, &r, &bits, &counts, &offsets, &src, &dest};
     return status_of(hipLaunchKernel(k, dim3((uint32_t)blocks), dim3(mxq::kSortThreads), args,
-                                     4 * e * (mxq::kSortWaves + 3), stream));
+                                     4 * (e * mxq::kSortWaves + pitch * 3), stream));
 }
 
 // ---- gather and quantize ---------------------------------------------------
@@ -225,8 +231,8 @@ size_t mxq_moe_sort_workspace_bytes(int64_t tokens, int64_t slots, int64_t exper
 {
     if (check_pairs(tokens, slots) != MXQ_OK || experts < 1 || experts > MXQ_MOE_MAX_EXPERTS)
         return 0;
-    const int64_t blocks = sort_blocks(tokens * slots);
-    return blocks > 1 ? (size_t)(blocks * experts * 4) : 0;
+    const int64_t blocks = sort_blocks(tokens * slots, experts);
+    return blocks > 1 ? (size_t)(blocks * ((experts + 3) / 4 * 4) * 4) : 0;
 }
 
 int mxq_moe_sort(const void *ids, int id_bytes, int64_t tokens, int64_t slots, int64_t experts, int64_t align,

@@ -62,47 +62,68 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t lane)
     return v;
 }
 
-// Counts of this wave's part [first, last) of the pairs into row[0 .. experts).
+// A wave takes its part in batches of 4 pairs per lane, loaded together; with
+// one batch (chunks of up to kSortBatch pairs) the counting's keys are kept for
+// the placing.
+constexpr uint32_t kSortKeys = 4;
+constexpr uint32_t kSortBatch = kSortKeys * kSortThreads;
+
 template <typename ID>
-__device__ __forceinline__ void sort_count(const ID *ids, uint32_t first, uint32_t last, uint32_t pairs,
-                                           uint32_t experts, uint32_t lane, uint32_t *row)
+__device__ __forceinline__ void sort_load(const ID *ids, uint32_t first, uint32_t pairs, uint32_t experts,
+                                          uint32_t lane, uint32_t (&key)[kSortKeys])
 {
-    for (uint32_t p = first; p < last; p += 64) {
-        const uint32_t key = sort_key(ids, p + lane, pairs, experts);
-        if (key < experts)
-            atomicAdd(row + key, 1u);
+#pragma unroll
+    for (uint32_t k = 0; k < kSortKeys; k++)
+        key[k] = sort_key(ids, first + 64u * k + lane, pairs, experts);
+}
+
+// Counts of this wave's part, `key` its first batch, into row[0 .. experts).
+template <typename ID>
+__device__ __forceinline__ void sort_count(const ID *ids, uint32_t first, uint32_t part, uint32_t pairs,
+                                           uint32_t experts, uint32_t lane, uint32_t (&key)[kSortKeys], uint32_t *row)
+{
+    for (uint32_t p = 0; p < part; p += 64 * kSortKeys) {
+        if (p > 0)
+            sort_load(ids, first + p, pairs, experts, lane, key);
+#pragma unroll
+        for (uint32_t k = 0; k < kSortKeys; k++)
+            if (key[k] < experts && p + 64u * k < part)
+                atomicAdd(row + key[k], 1u);
     }
 }
 
-// Launch 1 of 2: counts[block][expert] of each workgroup's chunk. The 16 waves
-// share one row of LDS counts.
+// Launch 1 of 2: counts[block][expert] of each workgroup's chunk, in rows of
+// `pitch` (experts rounded up to 4, the rest zero). The 16 waves share one row
+// of LDS counts.
 template <typename ID>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const ID *__restrict__ ids, uint32_t pairs,
-                                                                  uint32_t chunk, uint32_t experts,
+                                                                  uint32_t chunk, uint32_t experts, uint32_t pitch,
                                                                   uint32_t *__restrict__ counts)
 {
     extern __shared__ uint32_t row[];
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-    for (uint32_t e = tid; e < experts; e += kSortThreads)
-        row[e] = 0;
-    __syncthreads();
     const uint32_t part = chunk / kSortWaves;
     const uint32_t first = blockIdx.x * chunk + wave * part;
-    sort_count(ids, first, first + part, pairs, experts, lane, row);
+    uint32_t key[kSortKeys];
+    sort_load(ids, first, pairs, experts, lane, key);
+    for (uint32_t e = tid; e < pitch; e += kSortThreads)
+        row[e] = 0;
     __syncthreads();
-    for (uint32_t e = tid; e < experts; e += kSortThreads)
-        counts[(uint64_t)blockIdx.x * experts + e] = row[e];
+    sort_count(ids, first, part, pairs, experts, lane, key, row);
+    __syncthreads();
+    for (uint32_t e = tid; e < pitch; e += kSortThreads)
+        counts[(uint64_t)blockIdx.x * pitch + e] = row[e];
 }
 
 // Launch 2 of 2 (SINGLE = 0), or the whole sort in one workgroup (SINGLE = 1,
 // no counts in memory). Chunks are multiples of 64 * kSortWaves pairs and
 // blocks * chunk < 2^32 (checked on the host).
-//   LDS: kSortWaves rows of counts, then 3 arrays of experts: each group's
+//   LDS: kSortWaves rows of counts, then 3 arrays of `pitch`: each group's
 //   pairs, the pairs of it before this chunk, its first row
 template <typename ID, int SINGLE>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const ID *__restrict__ ids, uint32_t pairs,
-                                                                  uint32_t chunk, uint32_t experts, uint32_t align,
-                                                                  uint32_t rows, uint32_t key_bits,
+                                                                  uint32_t chunk, uint32_t experts, uint32_t pitch,
+                                                                  uint32_t align, uint32_t rows, uint32_t key_bits,
                                                                   const uint32_t *__restrict__ counts,
                                                                   int32_t *__restrict__ offsets,
                                                                   int32_t *__restrict__ src,
@@ -110,47 +131,53 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const ID *__re
 {
     extern __shared__ uint32_t lds[];
     __shared__ uint32_t wave_total[kSortWaves];
-    uint32_t *total = lds + kSortWaves * experts, *before = total + experts, *start = before + experts;
+    uint32_t *total = lds + kSortWaves * experts, *before = total + pitch, *start = before + pitch;
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
     const uint32_t blocks = gridDim.x, block = blockIdx.x;
-
-    for (uint32_t n = tid; n < (kSortWaves + 2) * experts; n += kSortThreads)
-        lds[n] = 0;
-    __syncthreads();
     const uint32_t part = chunk / kSortWaves;
     const uint32_t first = block * chunk + wave * part;
+    uint32_t key[kSortKeys];
+    sort_load(ids, first, pairs, experts, lane, key);
+
+    for (uint32_t n = tid; n < kSortWaves * experts + 2 * pitch; n += kSortThreads)
+        lds[n] = 0;
+    __syncthreads();
     uint32_t *mine = lds + wave * experts;
-    sort_count(ids, first, first + part, pairs, experts, lane, mine);
+    sort_count(ids, first, part, pairs, experts, lane, key, mine);
     if constexpr (!SINGLE) {
-        // the workgroup's threads as rows of `width` experts: each row sums
-        // its share of the chunks
-        uint32_t width = 64;
-        while (width < experts)
+        // the workgroup's threads as rows of `width`, 4 experts each: each row
+        // sums its share of the chunks
+        uint32_t width = 16;
+        while (4u * width < experts)
             width <<= 1;
-        const uint32_t e = tid & (width - 1), r = tid / width, n = kSortThreads / width;
-        uint32_t all = 0, prior = 0;
-        if (e < experts) {
+        const uint32_t e = 4u * (tid & (width - 1)), r = tid / width, n = kSortThreads / width;
+        u32x4_t all = {0u, 0u, 0u, 0u}, prior = all;
+        if (e < pitch) {
 #pragma unroll 8
             for (uint32_t b = r; b < blocks; b += n) {
-                const uint32_t c = counts[(uint64_t)b * experts + e];
+                const u32x4_t c = *reinterpret_cast<const u32x4_t *>(counts + (uint64_t)b * pitch + e);
                 all += c;
-                prior += b < block ? c : 0u;
+                prior += b < block ? c : u32x4_t{0u, 0u, 0u, 0u};
             }
-            atomicAdd(total + e, all);
-            atomicAdd(before + e, prior);
+#pragma unroll
+            for (uint32_t k = 0; k < 4; k++) {
+                atomicAdd(total + e + k, all[k]);
+                atomicAdd(before + e + k, prior[k]);
+            }
         }
     }
     __syncthreads();
 
     // thread e: group e's size, then the groups' first rows by a scan
     const uint32_t e = tid;
-    uint32_t sum = 0;
+    uint32_t sum = 0, c[kSortWaves] = {};
     if (e < experts) {
-        for (uint32_t w = 0; w < kSortWaves; w++) {
-            const uint32_t c = lds[w * experts + e];
-            lds[w * experts + e] = sum;   // pairs of this chunk before wave w
-            sum += c;
-        }
+#pragma unroll
+        for (uint32_t w = 0; w < kSortWaves; w++)
+            c[w] = lds[w * experts + e];
+#pragma unroll
+        for (uint32_t w = 0; w < kSortWaves; w++)
+            sum += c[w];
         if constexpr (SINGLE)
             total[e] = sum;
         else
@@ -167,9 +194,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const ID *__re
     if (e < experts) {
         const uint32_t at = base + scan - padded;
         start[e] = at;
-        const uint32_t here = at + before[e];
-        for (uint32_t w = 0; w < kSortWaves; w++)
-            lds[w * experts + e] += here;
+        uint32_t here = at + before[e];   // the chunk's first row of group e, then each wave's
+#pragma unroll
+        for (uint32_t w = 0; w < kSortWaves; w++) {
+            lds[w * experts + e] = here;
+            here += c[w];
+        }
         if (block == 0) {
             offsets[e] = (int32_t)at;
             if (e + 1 == experts)
@@ -178,24 +208,30 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const ID *__re
     }
     __syncthreads();
 
-    for (uint32_t p = first; p < first + part && p < pairs; p += 64) {
-        const uint32_t pair = p + lane;
-        const uint32_t key = sort_key(ids, pair, pairs, experts);
-        uint64_t same = __ballot(key < experts);
-        for (uint32_t b = 0; b < key_bits; b++) {
-            const uint64_t set = __ballot((key >> b) & 1u);
-            same &= (key >> b) & 1u ? set : ~set;
-        }
-        uint32_t row = 0;
-        const uint32_t leader = same ? (uint32_t)__builtin_ctzll(same) : lane;
-        if (key < experts && lane == leader)
-            row = atomicAdd(mine + key, (uint32_t)__popcll(same));
-        row = (uint32_t)__shfl((int)row, (int)leader) +
-              (uint32_t)__popcll(same & ((1ull << lane) - 1ull));
-        if (pair < pairs) {
-            dest[pair] = key < experts ? (int32_t)row : -1;
-            if (key < experts && row < rows)
-                src[row] = (int32_t)pair;
+    for (uint32_t p = 0; p < part && first + p < pairs; p += 64 * kSortKeys) {
+        if (part > 64 * kSortKeys)
+            sort_load(ids, first + p, pairs, experts, lane, key);
+#pragma unroll
+        for (uint32_t k = 0; k < kSortKeys; k++) {
+            const uint32_t pair = first + p + 64u * k + lane;
+            if (p + 64u * k >= part)
+                break;
+            uint64_t same = __ballot(key[k] < experts);
+            for (uint32_t b = 0; b < key_bits; b++) {
+                const uint64_t set = __ballot((key[k] >> b) & 1u);
+                same &= (key[k] >> b) & 1u ? set : ~set;
+            }
+            uint32_t row = 0;
+            const uint32_t leader = same ? (uint32_t)__builtin_ctzll(same) : lane;
+            if (key[k] < experts && lane == leader)
+                row = atomicAdd(mine + key[k], (uint32_t)__popcll(same));
+            row = (uint32_t)__shfl((int)row, (int)leader) +
+                  (uint32_t)__popcll(same & ((1ull << lane) - 1ull));
+            if (pair < pairs) {
+                dest[pair] = key[k] < experts ? (int32_t)row : -1;
+                if (key[k] < experts && row < rows)
+                    src[row] = (int32_t)pair;
+            }
         }
     }
     // rows without a pair: a wave per group, then past the last group
