@@ -8,22 +8,6 @@
 #include "mxq_host.hpp"
 #include "mxq_grouped_kernels.hpp"
 
-#ifndef M1
-#define M1 96
-#endif
-#ifndef M2
-#define M2 96
-#endif
-#ifndef XCW
-#define XCW 2
-#define XKW 2
-#endif
-#ifndef SD1
-#define SD1 2
-#endif
-#ifndef SD2
-#define SD2 2
-#endif
 namespace {
 
 using mxq_host::grid_fits;
@@ -36,8 +20,9 @@ template <int FMT, int EPI> grouped_fn pick_kernel(int kind)
     switch (kind) {
     case 0: return mxq::grouped_matmul_kernel<FMT, EPI, mxq::kGroupRows>;
     case 1: return mxq::grouped_matmul_kernel<FMT, EPI, mxq::kGroupWgrad>;
-    case 2: return mxq::grouped_stream_kernel<FMT, EPI, 1, XCW, XKW, SD1>;
-    default: return mxq::grouped_stream_kernel<FMT, EPI, 2, 1, 4, SD2>;
+    case 2: return mxq::grouped_mid_kernel<FMT, EPI>;
+    case 3: return mxq::grouped_stream_kernel<FMT, EPI, 2, 2>;
+    default: return mxq::grouped_stream_kernel<FMT, EPI, 1, 4>;
     }
 }
 
@@ -103,13 +88,24 @@ int mxq_grouped_matmul(const void *lhs, const void *lhs_scale, const void *rhs, 
         return rc;
     // Row tiles of any grouping of the rows: every group (and the rows past
     // the last one) may end with a part of a tile. The tile follows from the
-    // mean rows per group.
+    // mean rows per group (a weight of 4096 x 4096 or 2048 x 2048 e4m3fn, 268 MB
+    // of them, us):
+    //                      32-row tiles  128-row tiles  256-row tiles
+    //   64                      57           62-71           79
+    //   128                    90-92         60-74          76-81
+    //   2048 (4096 x 4096)       -           547             500
     const int64_t mean = rows / groups;
-    const int kind = mean <= M1 ? 2 : mean <= M2 ? 3 : 0;
-    const int64_t tile = kind == 2 ? 32 : kind == 3 ? 64 : mxq::kMmTile;
-    const int64_t cols = kind == 2 ? XCW * mxq::kStreamCols : kind ? mxq::kStreamCols : mxq::kMmTile;
-    const uint32_t threads = kind ? kind == 2 ? 64 * XCW * XKW : 256 : mxq::kMmThreads;
-    const int64_t tiles_m = rows / tile + groups + 1, tiles_n = (N + cols - 1) / cols;
+    int kind = mean <= 96 ? 3 : mean <= 256 ? 2 : 0;
+    const int64_t tile = kind == 3 ? mxq::kStreamRows : kind == 2 ? mxq::kMidRows : mxq::kMmTile;
+    const int64_t tiles_m = rows / tile + groups + 1;
+    int64_t tiles_n = (N + mxq::kMmTile - 1) / mxq::kMmTile;
+    const uint32_t threads = kind ? 256 : mxq::kMmThreads;
+    // with few tiles, narrower ones whose four waves all share the contraction
+    // (8 experts x 32 rows, 4096 x 4096: 33 -> 28 us; 16 x 64 rows: 57 -> 92)
+    if (kind == 3 && (rows + tile - 1) / tile * tiles_n < 384) {
+        kind = 4;
+        tiles_n = (N + mxq::kStreamCols - 1) / mxq::kStreamCols;
+    }
     if (!grid_fits(tiles_m, tiles_n, threads))
         return MXQ_E_OVERFLOW;
     return launch(pick(fmt, res_dtype, kind), tiles_m * tiles_n, threads, lhs, lhs_scale, rhs, rhs_scale, offsets,
