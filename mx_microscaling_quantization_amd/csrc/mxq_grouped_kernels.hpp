@@ -47,7 +47,8 @@ __device__ __forceinline__ void group_bounds(const int32_t *offsets, uint32_t gr
 // `per` consecutive groups (the rows past the last one count as a group), a
 // scan over the lanes gives each lane's first tile and the number of tiles.
 struct GroupScan {
-    uint32_t per, first, total;   // groups per lane; this lane's first row tile; all row tiles
+    uint32_t per, first;    // groups per lane; this lane's first row tile
+    uint32_t real, total;   // row tiles of the groups; with those past the last group
 };
 
 template <uint32_t TILE>
@@ -72,6 +73,9 @@ __device__ __forceinline__ GroupScan group_scan(const int32_t *offsets, uint32_t
     }
     s.first = v - n;
     s.total = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+    uint32_t a, b;
+    group_bounds(offsets, groups, R, groups, a, b);
+    s.real = s.total - (uint32_t)__builtin_amdgcn_readfirstlane((int)((b - a + TILE - 1) / TILE));
     return s;
 }
 
@@ -112,6 +116,32 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t w, uint32_t n)
     if (w / kMmXcds < q)
         return (w % kMmXcds) * q + w / kMmXcds;
     return w;   // the tail: w >= 8 q, in place
+}
+
+// Row and column tile of workgroup w; false if there is none. The groups' tiles
+// are walked in sets of WALK tile rows column by column, so that the workgroups
+// an XCD runs at a time share operand panels; the tiles past the last group,
+// which only store zeros, come after them and are not part of the XCDs' even
+// shares (64 experts, 62 of them used, x 32 rows, 4096 x 2048: with them some XCDs
+// got 70 products for their 64 places, 101 us).
+template <uint32_t WALK>
+__device__ __forceinline__ bool grouped_tile(const GroupScan &s, uint32_t tiles_n, uint32_t &row, uint32_t &col)
+{
+    const uint32_t real = s.real * tiles_n;
+    const uint32_t t = xcd_tile(blockIdx.x, real);
+    if (t >= s.total * tiles_n)
+        return false;
+    if (t >= real) {
+        row = t / tiles_n;
+        col = t - row * tiles_n;
+        return true;
+    }
+    const uint32_t walk = t / (WALK * tiles_n);
+    const uint32_t rows = min(WALK, s.real - walk * WALK);
+    const uint32_t in_walk = t - walk * WALK * tiles_n;
+    col = in_walk / rows;
+    row = walk * WALK + in_walk - col * rows;
+    return true;
 }
 
 // ----------------------------------------------------------------------------
@@ -218,16 +248,12 @@ __global__ __launch_bounds__(kMmThreads) void grouped_matmul_kernel(
         // M sorted rows, P operand rows. Tile rows of all groups in order,
         // walked in fours column by column as the scaled matmul does.
         const GroupScan s = group_scan<kMmTile>(offsets, groups, M, lane);
-        const uint32_t t = xcd_tile(blockIdx.x, s.total * tiles_n);
-        if (t >= s.total * tiles_n)
+        uint32_t row, col;
+        if (!grouped_tile<kMmGroupRows>(s, tiles_n, row, col))
             return;
-        const uint32_t walk = t / (kMmGroupRows * tiles_n);
-        const uint32_t first_row = walk * kMmGroupRows;
-        const uint32_t rows = min((uint32_t)kMmGroupRows, s.total - first_row);
-        const uint32_t in_walk = t - walk * kMmGroupRows * tiles_n;
-        const GroupTile g = group_find<kMmTile>(offsets, groups, M, s, first_row + in_walk % rows);
+        const GroupTile g = group_find<kMmTile>(offsets, groups, M, s, row);
         m0 = g.m0;
-        n0 = in_walk / rows * kMmTile;
+        n0 = col * kMmTile;
         row_end = g.end;
         if (g.group >= groups) {
             P = 0;   // no operand rows: the product is zero
@@ -331,15 +357,11 @@ __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
     const uint32_t i = lane & 31u, h = lane >> 5;
 
     const GroupScan sc = group_scan<kMidRows>(offsets, groups, M, lane);
-    const uint32_t t = xcd_tile(blockIdx.x, sc.total * tiles_n);
-    if (t >= sc.total * tiles_n)
+    uint32_t row, col;
+    if (!grouped_tile<2 * kMmGroupRows>(sc, tiles_n, row, col))
         return;
-    const uint32_t walk = t / (2 * kMmGroupRows * tiles_n);
-    const uint32_t first_row = walk * 2 * kMmGroupRows;
-    const uint32_t rows = min((uint32_t)(2 * kMmGroupRows), sc.total - first_row);
-    const uint32_t in_walk = t - walk * 2 * kMmGroupRows * tiles_n;
-    const GroupTile g = group_find<kMidRows>(offsets, groups, M, sc, first_row + in_walk % rows);
-    const uint32_t n0 = in_walk / rows * kMmTile;
+    const GroupTile g = group_find<kMidRows>(offsets, groups, M, sc, row);
+    const uint32_t n0 = col * kMmTile;
     if (g.group >= groups) {
         P = 0;
     } else {
@@ -576,12 +598,11 @@ __global__ __launch_bounds__(64 * CW * KW, 2) void grouped_stream_kernel(
     const uint32_t i = lane & 31u, h = lane >> 5;
 
     const GroupScan sc = group_scan<kStreamRows>(offsets, groups, M, lane);
-    const uint32_t t = xcd_tile(blockIdx.x, sc.total * tiles_n);
-    if (t >= sc.total * tiles_n)
+    uint32_t row, col;
+    if (!grouped_tile<1>(sc, tiles_n, row, col))
         return;
-    const uint32_t tr = t / tiles_n;
-    const GroupTile g = group_find<kStreamRows>(offsets, groups, M, sc, tr);
-    const uint32_t n0 = ((t - tr * tiles_n) * CW + cw) * kStreamCols;
+    const GroupTile g = group_find<kStreamRows>(offsets, groups, M, sc, row);
+    const uint32_t n0 = (col * CW + cw) * kStreamCols;
     if (g.group >= groups) {
         P = 0;
     } else {
