@@ -202,15 +202,19 @@ __device__ __forceinline__ void grouped_results(const f32x16_t (&acc)[2][4], con
                                                 uint32_t wm0, uint32_t wn0, uint32_t row_end, uint32_t i, uint32_t h,
                                                 void *out)
 {
-    bool finite = true;
+    // 0 times a finite sum is a zero, of anything else a NaN that stays: one
+    // instruction per sum, in eight chains (a class test per sum and the scalar
+    // logic to collect them took 0.7 us more per tile)
+    float zero[8] = {};
 #pragma unroll
     for (int a = 0; a < 2; a++)
 #pragma unroll
         for (int u = 0; u < 4; u++)
 #pragma unroll
             for (int r = 0; r < 16; r++)
-                finite = finite && __builtin_isfinite(acc[a][u][r]);
-    if (wave_any(!finite)) {
+                zero[4 * a + u] = __builtin_fmaf(acc[a][u][r], 0.0f, zero[4 * a + u]);
+    const float all = ((zero[0] + zero[1]) + (zero[2] + zero[3])) + ((zero[4] + zero[5]) + (zero[6] + zero[7]));
+    if (wave_any(!(all == 0.0f))) {
         mm_rare_part<F, EPI>(lhs, lhs_scale, rhs, rhs_scale, P, M, N, wm0, wn0, 1u, out, nullptr, 0, row_end);
         return;
     }
