@@ -126,7 +126,6 @@ __device__ __forceinline__ void mm_source(MmSource &s, const uint8_t *data, cons
 // as zero; a step at or past row P gets an empty range and touches no
 // memory. Columns past C read bytes of the next row (or zeros); they only
 // reach results outside the output.
-template <int AUX = 0>
 __device__ __forceinline__ void mm_copy_quad(const MmSource &s, uint8_t *tile, uint32_t P, uint32_t step,
                                               uint32_t quad, uint32_t lane)
 {
@@ -140,7 +139,7 @@ __device__ __forceinline__ void mm_copy_quad(const MmSource &s, uint8_t *tile, u
 #pragma unroll
     for (uint32_t v = 0; v < 4; v++)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_void_t *)(tile + kMmQuadPitch * quad + 1024u * v), 16,
-                                                 16u * lane, q0 + v * s.pitch, 0, AUX);
+                                                 16u * lane, q0 + v * s.pitch, 0, 0);
 }
 
 // E8M0 row of K block kb (256 containers from c0) -> `stile` (LDS); blocks
