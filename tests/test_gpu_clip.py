@@ -154,3 +154,13 @@ def test_stream_graph_and_repeats():
         torch.cuda.synchronize()
         assert torch.equal(n, want_norm) and all(torch.equal(a, b) for a, b in zip(out, want))
         _ = ts[3].float().sum().item()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_large_tensors(in_place):
+    """More tiles than the scaling adds the partial sums for by itself (128 MiB),
+    alone and with more tensors than one launch holds."""
+    big = [torch.randn(50_000_003, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16),
+           rand(17_000_001, torch.float32, 2)]
+    check(big, 0.3, in_place)
+    check(big + [rand(1 + 37 * i, TYPES[i % 3], i) for i in range(130)], 0.3, in_place)

@@ -296,3 +296,55 @@ def test_other_stream_graph_and_repeats():
         torch.cuda.synchronize()
         assert torch.equal(a, want) and torch.equal(b, want_w)
         _ = (a.float() * 2).sum().item()
+
+
+# ---- each form of the product, by the rule that picks it -------------------------
+
+def test_two_column_waves():
+    """Few rows per group and enough tiles (rows / 32 times N / 256 from 384 on):
+    two waves side by side, the last of them past the last column."""
+    g = np.random.default_rng(7)
+    sizes = (32 * g.integers(0, 3, size=64)).tolist()
+    sizes += [32] * ((2048 - sum(sizes)) // 32)
+    progress("grouped rows, 2 x 2 waves, %d groups" % len(sizes))
+    check_rows(sizes, 64, 96, 1544, "e4m3fn", torch.bfloat16, seed=5)
+    check_rows(sizes, 64, 224, 1668, "e5m2", torch.float32, seed=6)
+
+    def patch(l, ls, r, rs):
+        ls[1, 40:50] = 255
+        rs[:, 1, :] = 15
+        rs[3, 0, ::7] = 255
+        ls[0, :] = 12
+
+    check_rows(sizes, 64, 96, 1544, "e4m3fn", torch.float32, seed=8, patch=patch, per_block=4)
+
+
+@pytest.mark.parametrize("sizes", [[128, 160, 132], [100, 256, 40, 300], [4, 500, 128]])
+@pytest.mark.parametrize("res", [torch.float32, torch.bfloat16])
+def test_middling_groups_rare_path(sizes, res):
+    """97 to 256 rows per group on average: 128-row tiles, with scale bytes of 255
+    and NaN codes in them."""
+    def scales(l, ls, r, rs):
+        ls[1, 3:150] = 255
+        rs[:, 1, :] = 20
+        rs[:, 0, ::5] = 255
+        ls[0, :] = 14
+
+    def codes(l, ls, r, rs):
+        l[3, 4 * 130 + 2] = 0x7F
+        r[1, 2, 4 * 17 + 1] = 0xFF
+
+    progress("grouped rows, 128-row tiles %s %s" % (sizes, res))
+    check_rows(sizes, 20, 160, 300, "e4m3fn", res)
+    check_rows(sizes, 20, 160, 300, "e4m3fn", res, patch=scales, per_block=4)
+    check_rows(sizes, 20, 96, 132, "e4m3fn", res, patch=codes, per_block=4)
+
+
+@pytest.mark.parametrize("mean", [140, 300])
+def test_many_groups_of_many_rows(mean):
+    """More groups than lanes of a wave, for the 128- and 256-row tiles."""
+    g = np.random.default_rng(mean)
+    sizes = (4 * g.integers(mean // 8, mean * 3 // 8, size=70)).tolist()
+    sizes[3] = sizes[66] = 0
+    progress("grouped rows, 70 groups of about %d" % mean)
+    check_rows(sizes, 96, 64, 68, "e4m3fn", torch.bfloat16, seed=mean)

@@ -354,3 +354,34 @@ def test_graph_capture(T):
         for n, (a, b) in enumerate(zip(outs, step())):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), "replay %d output %d" % (rep, n)
         _ = (x.float() * 2).sum().item()
+
+
+# ---- each form, by the rule that picks it -------------------------------------
+
+@pytest.mark.parametrize("in_dtype,fmt", [("bf16", "e4m3fn"), ("f16", "e2m1"), ("f16", "e5m2")])
+@pytest.mark.parametrize("T,k,K", [(4100, 2, 4100), (5001, 3, 3460), (300, 2, 520), (8200, 2, 2100)])
+def test_gather_quantize_down_orders(T, k, K, in_dtype, fmt):
+    """Tiles numbered run by run (x over 32 MiB, up to 8192 tokens, more than one
+    slot) and band by band, against quantize_axis on the gathered rows."""
+    progress("gather_quantize dim=-2 T=%d k=%d K=%d %s->%s" % (T, k, K, in_dtype, fmt))
+    plan = plan_of(make_ids(T, k, 24, T), 24)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    x = (torch.randn((T, K), generator=g, device="cuda") * 3).to(IN_T[in_dtype])
+    rows = torch.where(plan.src[:, None] >= 0, x[plan.src.clamp(min=0).long() // k], torch.zeros((), dtype=x.dtype,
+                                                                                                  device="cuda"))
+    got = mxq.moe_gather_quantize(x, plan, fmt, dim=-2)
+    want = mxq.quantize_axis(rows, fmt, -2, dense_scale=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T,k,K", [(3000, 4, 2080), (9001, 2, 96)])
+def test_gather_quantize_along_many_tiles(T, k, K):
+    plan = plan_of(make_ids(T, k, 24, T), 24)
+    x = torch.randn((T, K), device="cuda").to(torch.bfloat16)
+    rows = torch.where(plan.src[:, None] >= 0, x[plan.src.clamp(min=0).long() // k], torch.zeros((), dtype=x.dtype,
+                                                                                                  device="cuda"))
+    for fmt in ("e4m3fn", "e2m1"):
+        got = mxq.moe_gather_quantize(x, plan, fmt)
+        want = mxq.quantize_axis(rows, fmt, -1, dense_scale=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
