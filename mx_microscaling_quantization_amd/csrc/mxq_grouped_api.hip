@@ -20,7 +20,8 @@ template <int FMT, int EPI> grouped_fn pick_kernel(int kind)
     switch (kind) {
     case 0: return mxq::grouped_matmul_kernel<FMT, EPI, mxq::kGroupRows>;
     case 1: return mxq::grouped_matmul_kernel<FMT, EPI, mxq::kGroupWgrad>;
-    case 2: return mxq::grouped_mid_kernel<FMT, EPI>;
+    case 2: return mxq::grouped_mid_kernel<FMT, EPI, mxq::kGroupRows>;
+    case 5: return mxq::grouped_mid_kernel<FMT, EPI, mxq::kGroupWgrad>;
     case 3: return mxq::grouped_stream_kernel<FMT, EPI, 2, 2>;
     default: return mxq::grouped_stream_kernel<FMT, EPI, 1, 4>;
     }
@@ -86,26 +87,42 @@ int mxq_grouped_matmul(const void *lhs, const void *lhs_scale, const void *rhs, 
     const int rc = check(lhs, lhs_scale, rhs, rhs_scale, offsets, groups, P, rows, N, fmt, res_dtype, out, P == 0);
     if (rc != MXQ_OK || rows == 0 || N == 0)
         return rc;
-    // Row tiles of any grouping of the rows: every group (and the rows past
-    // the last one) may end with a part of a tile. The tile follows from the
-    // mean rows per group (a weight of 4096 x 4096 or 2048 x 2048 e4m3fn, 268 MB
-    // of them, us):
-    //                      32-row tiles  128-row tiles  256-row tiles
+    // The tile follows from the mean rows per group, the length of the
+    // contraction and the number of tiles (a weight of 4096 x 4096 or
+    // 2048 x 2048 e4m3fn, 268 MB of them, us):
+    //   rows per group      32-row tiles  128-row tiles  256-row tiles
     //   64                      57           62-71           79
     //   128                    90-92         60-74          76-81
+    //   350 (4096 x 4096)        -           124             127
+    //   414 (4096 x 2048)        -            68              65
     //   2048 (4096 x 4096)       -           547             500
-    const int64_t mean = rows / groups;
-    int kind = mean <= 96 ? 3 : mean <= 256 ? 2 : 0;
-    const int64_t tile = kind == 3 ? mxq::kStreamRows : kind == 2 ? mxq::kMidRows : mxq::kMmTile;
-    const int64_t tiles_m = rows / tile + groups + 1;
-    int64_t tiles_n = (N + mxq::kMmTile - 1) / mxq::kMmTile;
-    const uint32_t threads = kind ? 256 : mxq::kMmThreads;
-    // with few tiles, narrower ones whose four waves all share the contraction
-    // (8 experts x 32 rows, 4096 x 4096: 33 -> 28 us; 16 x 64 rows: 57 -> 92)
-    if (kind == 3 && (rows + tile - 1) / tile * tiles_n < 384) {
+    // A short contraction is mostly the stores of its results, which several
+    // smaller workgroups on a CU overlap with other tiles' products (16 experts,
+    // 32768 rows, 4096 columns: 64 values 63 us, 256-row tiles 73; 512 values
+    // 121 and 128; 1024 values equal; 2048 values 297 and 285).
+    // Where 128-row tiles do not fill half of the CUs, the time is one tile's
+    // whole contraction, which the small ones share out among their waves
+    // (512 x 4096 by 4096 x 4096: 24 us and 46; with 182 such tiles, 1536 rows
+    // over 2048 values by 3584 columns: 32 and 28).
+    const int64_t mean = rows / groups, kCus = 256;
+    const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    int64_t tiles_n = up(N, mxq::kMmTile);
+    int kind = 0;
+    if (mean <= 96 || 2 * up(rows, mxq::kMidRows) * tiles_n <= kCus)
+        kind = 3;
+    else if (mean <= 384 || P <= 256)
+        kind = 2;
+    // with fewer small tiles than that, narrower ones whose four waves all share
+    // the contraction (8 experts x 32 rows, 4096 x 4096, 128 tiles: 24 us, wide
+    // ones 32; 2 x 64 rows, 4096 x 8192, 160 tiles: 31 and 28)
+    if (kind == 3 && 2 * up(rows, mxq::kStreamRows) * tiles_n <= kCus) {
         kind = 4;
-        tiles_n = (N + mxq::kStreamCols - 1) / mxq::kStreamCols;
+        tiles_n = up(N, mxq::kStreamCols);
     }
+    // every group, and the rows past the last one, may end with a part of a tile
+    const int64_t tile = kind >= 3 ? mxq::kStreamRows : kind == 2 ? mxq::kMidRows : mxq::kMmTile;
+    const int64_t tiles_m = rows / tile + groups + 1;
+    const uint32_t threads = kind ? 256 : mxq::kMmThreads;
     if (!grid_fits(tiles_m, tiles_n, threads))
         return MXQ_E_OVERFLOW;
     return launch(pick(fmt, res_dtype, kind), tiles_m * tiles_n, threads, lhs, lhs_scale, rhs, rhs_scale, offsets,
@@ -119,10 +136,19 @@ int mxq_grouped_matmul_wgrad(const void *lhs, const void *lhs_scale, const void 
     const int rc = check(lhs, lhs_scale, rhs, rhs_scale, offsets, groups, P, M, N, fmt, res_dtype, out, P == 0);
     if (rc != MXQ_OK || M == 0 || N == 0)
         return rc;
-    const int64_t tiles_m = (M + mxq::kMmTile - 1) / mxq::kMmTile, tiles_n = (N + mxq::kMmTile - 1) / mxq::kMmTile;
-    if (!grid_fits(tiles_m, tiles_n, mxq::kMmThreads) || !grid_fits(tiles_m * tiles_n, groups, mxq::kMmThreads))
+    // With little to multiply per group the time is that of writing the result,
+    // which several smaller workgroups on a CU overlap with the products of
+    // others (weight gradients of 2048 x 2048, 271 rows of the contraction per
+    // group: 78 us, 256-row tiles 84; 39 of 1920 x 768, 512 rows: 58 and 63;
+    // 35 of 672 x 3328, 1067 rows: 132 and 129; 16 of 2048 x 4096, 2064 rows:
+    // 293 and 276).
+    const bool mid = 4 * P / groups < 768;
+    const int64_t tile = mid ? mxq::kMidRows : mxq::kMmTile;
+    const uint32_t threads = mid ? mxq::kMidThreads : mxq::kMmThreads;
+    const int64_t tiles_m = (M + tile - 1) / tile, tiles_n = (N + mxq::kMmTile - 1) / mxq::kMmTile;
+    if (!grid_fits(tiles_m, tiles_n, threads) || !grid_fits(tiles_m * tiles_n, groups, threads))
         return MXQ_E_OVERFLOW;
-    return launch(pick(fmt, res_dtype, 1), tiles_m * tiles_n * groups, mxq::kMmThreads, lhs, lhs_scale, rhs,
+    return launch(pick(fmt, res_dtype, mid ? 5 : 1), tiles_m * tiles_n * groups, threads, lhs, lhs_scale, rhs,
                   rhs_scale, offsets, groups, P, M, N, tiles_n, out, stream);
 }
 

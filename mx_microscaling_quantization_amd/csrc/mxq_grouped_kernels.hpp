@@ -118,30 +118,110 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t w, uint32_t n)
     return w;   // the tail: w >= 8 q, in place
 }
 
-// Row and column tile of workgroup w; false if there is none. The groups' tiles
-// are walked in sets of WALK tile rows column by column, so that the workgroups
-// an XCD runs at a time share operand panels; the tiles past the last group,
-// which only store zeros, come after them and are not part of the XCDs' even
-// shares (64 experts, 62 of them used, x 32 rows, 4096 x 2048: with them some XCDs
-// got 70 products for their 64 places, 101 us).
-template <uint32_t WALK>
-__device__ __forceinline__ bool grouped_tile(const GroupScan &s, uint32_t tiles_n, uint32_t &row, uint32_t &col)
+// The 8-byte aligned `bytes` at p (a multiple of 8), share `index` of `count`
+// of them by this workgroup's threads, as zeros.
+__device__ __forceinline__ void zero_share(uint8_t *p, uint64_t bytes, uint32_t index, uint32_t count)
 {
-    const uint32_t real = s.real * tiles_n;
+    typedef uint32_t u32x4_8_t __attribute__((ext_vector_type(4), aligned(8)));
+    const uint64_t units = bytes / 16u;
+    const uint64_t end = units * (index + 1ull) / count;
+    for (uint64_t u = units * index / count + threadIdx.x; u < end; u += blockDim.x)
+        __builtin_nontemporal_store(u32x4_8_t{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4_8_t *>(p) + u);
+    if (index + 1 == count && threadIdx.x == 0 && bytes % 16u != 0)
+        *reinterpret_cast<u32x2_t *>(p + bytes - 8u) = u32x2_t{0u, 0u};
+}
+
+// A workgroup's tile: operands from their first row on, first output row and
+// column, the end of the output's rows.
+struct GroupedJob {
+    const uint8_t *lhs, *lhs_scale, *rhs, *rhs_scale;
+    uint8_t *out;
+    uint32_t P, m0, n0, row_end;
+    bool one_tile;    // (rows) the group has no other row tile
+};
+
+// Rows: the groups' tiles (TILE rows x COLS columns) are walked in sets of WALK
+// tile rows column by column, so that the workgroups an XCD runs at a time share
+// operand panels. The rows past the last group are cleared by further workgroups,
+// which are not part of the XCDs' even shares (64 experts, 62 of them used, x 32
+// rows, 4096 x 2048: with them some XCDs got 70 products for their 64 places, 101
+// us instead of 81). False: this workgroup has no product.
+template <uint32_t TILE, uint32_t COLS, uint32_t WALK, uint32_t ES>
+__device__ __forceinline__ bool rows_job(GroupedJob &job, const int32_t *offsets, uint32_t groups, uint32_t M,
+                                         uint32_t N, uint32_t tiles_n, uint32_t lane)
+{
+    const GroupScan s = group_scan<TILE>(offsets, groups, M, lane);
+    const uint32_t real = s.real * tiles_n, all = s.total * tiles_n;
     const uint32_t t = xcd_tile(blockIdx.x, real);
-    if (t >= s.total * tiles_n)
-        return false;
     if (t >= real) {
-        row = t / tiles_n;
-        col = t - row * tiles_n;
-        return true;
+        if (t < all) {
+            uint32_t a, b;
+            group_bounds(offsets, groups, M, groups, a, b);
+            zero_share(job.out + (uint64_t)a * N * ES, (uint64_t)(b - a) * N * ES, t - real, all - real);
+        }
+        return false;
     }
     const uint32_t walk = t / (WALK * tiles_n);
     const uint32_t rows = min(WALK, s.real - walk * WALK);
     const uint32_t in_walk = t - walk * WALK * tiles_n;
-    col = in_walk / rows;
-    row = walk * WALK + in_walk - col * rows;
+    const uint32_t col = in_walk / rows;
+    const GroupTile g = group_find<TILE>(offsets, groups, M, s, walk * WALK + in_walk - col * rows);
+    job.m0 = g.m0;
+    job.n0 = col * COLS;
+    job.row_end = g.end;
+    job.one_tile = g.end - g.first <= TILE;
+    job.rhs += (uint64_t)g.group * job.P * N * 4u;
+    job.rhs_scale += (uint64_t)g.group * (job.P / 8u) * N;
     return true;
+}
+
+// Wgrad: P operand rows in all, group g's are offsets[g] / 4 .. The tiles of one
+// group are spread over the XCDs (each gets consecutive ones), so that a large
+// group's work is. An empty group's result is cleared as one run of memory
+// instead of tile by tile (20 groups of 3264 x 3932, 18 of them empty: 240 us in
+// tiles).
+template <uint32_t TILE, uint32_t COLS, uint32_t WALK, uint32_t ES>
+__device__ __forceinline__ bool wgrad_job(GroupedJob &job, const int32_t *offsets, uint32_t groups, uint32_t M,
+                                          uint32_t N, uint32_t tiles_n)
+{
+    const uint32_t tiles_m = (M + TILE - 1) / TILE, per = tiles_m * tiles_n;
+    const uint32_t g = blockIdx.x / per;
+    const uint32_t t = xcd_tile(blockIdx.x - g * per, per);
+    uint32_t a, b;
+    group_bounds(offsets, groups, 4u * job.P, g, a, b);
+    a = __builtin_amdgcn_readfirstlane(a / 32u);   // whole blocks
+    b = __builtin_amdgcn_readfirstlane(b / 32u);
+    job.out += (uint64_t)g * M * N * ES;
+    if (a == b) {
+        zero_share(job.out, (uint64_t)M * N * ES, t, per);
+        return false;
+    }
+    const uint32_t walk = t / (WALK * tiles_n);
+    const uint32_t rows = min(WALK, tiles_m - walk * WALK);
+    const uint32_t in_walk = t - walk * WALK * tiles_n;
+    const uint32_t col = in_walk / rows;
+    job.m0 = (walk * WALK + in_walk - col * rows) * TILE;
+    job.n0 = col * COLS;
+    job.row_end = M;
+    job.one_tile = false;
+    job.lhs += (uint64_t)a * 8u * 4u * M;
+    job.lhs_scale += (uint64_t)a * M;
+    job.rhs += (uint64_t)a * 8u * 4u * N;
+    job.rhs_scale += (uint64_t)a * N;
+    job.P = (b - a) * 8u;
+    return true;
+}
+
+enum { kGroupRows = 0, kGroupWgrad = 1 };
+
+template <int MODE, uint32_t TILE, uint32_t COLS, uint32_t WALK, uint32_t ES>
+__device__ __forceinline__ bool grouped_job(GroupedJob &job, const int32_t *offsets, uint32_t groups, uint32_t M,
+                                            uint32_t N, uint32_t tiles_n, uint32_t lane)
+{
+    if constexpr (MODE == kGroupRows)
+        return rows_job<TILE, COLS, WALK, ES>(job, offsets, groups, M, N, tiles_n, lane);
+    else
+        return wgrad_job<TILE, COLS, WALK, ES>(job, offsets, groups, M, N, tiles_n);
 }
 
 // ----------------------------------------------------------------------------
@@ -161,7 +241,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 // col on; N % 4 == 0. A lane past the group's rows or the columns gives an
 // offset that the buffer's range check drops: no branch, so that the stores stay
 // in one block (see wave_any).
-template <int EPI, uint32_t HROWS>
+template <int EPI, uint32_t HROWS, int NT>
 __device__ __forceinline__ void grouped_store(const float *v, uint32_t m, uint32_t h, uint32_t row_end, uint32_t col,
                                               uint32_t N, void *__restrict__ out)
 {
@@ -174,10 +254,19 @@ __device__ __forceinline__ void grouped_store(const float *v, uint32_t m, uint32
     if constexpr (EPI == kEpiF32)
         __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]),
                                                        __float_as_uint(v[2]), __float_as_uint(v[3])},
-                                               rs, (int)at, 0, kBufferNT);
+                                               rs, (int)at, 0, NT ? kBufferNT : 0);
     else
         __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}, rs, (int)at, 0,
-                                              kBufferNT);
+                                              NT ? kBufferNT : 0);
+}
+
+// Whether rows of N results start on 128-byte lines. Their stores then have the
+// non-temporal hint (weight gradients of 2048 x 4096: 277 -> 262 us); otherwise two
+// tiles write parts of one line, which the hint keeps the L2 from putting
+// together (38 groups of 3296 x 2132: 155 us, 236 with it).
+template <int EPI> __device__ __forceinline__ bool whole_lines(uint32_t N)
+{
+    return N % (EPI == kEpiF32 ? 32u : 64u) == 0;
 }
 
 // Whether a lane's condition holds anywhere in the wave, as a scalar that the
@@ -192,15 +281,25 @@ __device__ __forceinline__ bool wave_any(bool lane_has)
     return __builtin_amdgcn_readfirstlane((uint32_t)m | (uint32_t)(m >> 32)) != 0;
 }
 
+template <int EPI, int NT>
+__device__ __forceinline__ void grouped_store_tile(const f32x16_t (&acc)[2][4], const GroupedJob &job, uint32_t N,
+                                                   uint32_t wm0, uint32_t col, uint32_t h)
+{
+#pragma unroll
+    for (int r = 0; r < 16; r++)
+#pragma unroll
+        for (int a = 0; a < 2; a++) {
+            const float v[4] = {acc[a][0][r], acc[a][1][r], acc[a][2][r], acc[a][3][r]};
+            grouped_store<EPI, 8, NT>(v, wm0 + 16u * (r >> 2) + 2u * (r & 3) + a, h, job.row_end, col, N, job.out);
+        }
+}
+
 // A wave's 64 x 128 sums from row wm0 and column wn0. Where one is not finite (a
 // scale byte of 255, or a sum that is not by itself) the wave computes its
 // part again on the scaled matmul's rare path.
 template <int F, int EPI>
-__device__ __forceinline__ void grouped_results(const f32x16_t (&acc)[2][4], const uint8_t *lhs,
-                                                const uint8_t *lhs_scale, const uint8_t *rhs,
-                                                const uint8_t *rhs_scale, uint32_t P, uint32_t M, uint32_t N,
-                                                uint32_t wm0, uint32_t wn0, uint32_t row_end, uint32_t i, uint32_t h,
-                                                void *out)
+__device__ __forceinline__ void grouped_results(const f32x16_t (&acc)[2][4], const GroupedJob &job, uint32_t M,
+                                                uint32_t N, uint32_t wm0, uint32_t wn0, uint32_t i, uint32_t h)
 {
     // 0 times a finite sum is a zero, of anything else a NaN that stays: one
     // instruction per sum, in eight chains (a class test per sum and the scalar
@@ -215,23 +314,19 @@ __device__ __forceinline__ void grouped_results(const f32x16_t (&acc)[2][4], con
                 zero[4 * a + u] = __builtin_fmaf(acc[a][u][r], 0.0f, zero[4 * a + u]);
     const float all = ((zero[0] + zero[1]) + (zero[2] + zero[3])) + ((zero[4] + zero[5]) + (zero[6] + zero[7]));
     if (wave_any(!(all == 0.0f))) {
-        mm_rare_part<F, EPI>(lhs, lhs_scale, rhs, rhs_scale, P, M, N, wm0, wn0, 1u, out, nullptr, 0, row_end);
+        mm_rare_part<F, EPI>(job.lhs, job.lhs_scale, job.rhs, job.rhs_scale, job.P, M, N, wm0, wn0, 1u, job.out,
+                             nullptr, 0, job.row_end);
         return;
     }
-#pragma unroll
-    for (int r = 0; r < 16; r++)
-#pragma unroll
-        for (int a = 0; a < 2; a++) {
-            const float v[4] = {acc[a][0][r], acc[a][1][r], acc[a][2][r], acc[a][3][r]};
-            grouped_store<EPI, 8>(v, wm0 + 16u * (r >> 2) + 2u * (r & 3) + a, h, row_end, wn0 + 4u * i, N, out);
-        }
+    if (whole_lines<EPI>(N))
+        grouped_store_tile<EPI, 1>(acc, job, N, wm0, wn0 + 4u * i, h);
+    else
+        grouped_store_tile<EPI, 0>(acc, job, N, wm0, wn0 + 4u * i, h);
 }
 
 // ----------------------------------------------------------------------------
 // Many rows per group: the scaled matmul's 256 x 256 tile
 // ----------------------------------------------------------------------------
-
-enum { kGroupRows = 0, kGroupWgrad = 1 };
 
 template <int FMT, int EPI, int MODE>
 __global__ __launch_bounds__(kMmThreads) void grouped_matmul_kernel(
@@ -247,57 +342,14 @@ __global__ __launch_bounds__(kMmThreads) void grouped_matmul_kernel(
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t grp = wave >> 2, wq = wave & 3u;
 
-    uint32_t m0, n0, row_end;
-    if constexpr (MODE == kGroupRows) {
-        // M sorted rows, P operand rows. Tile rows of all groups in order,
-        // walked in fours column by column as the scaled matmul does.
-        const GroupScan s = group_scan<kMmTile>(offsets, groups, M, lane);
-        uint32_t row, col;
-        if (!grouped_tile<kMmGroupRows>(s, tiles_n, row, col))
-            return;
-        const GroupTile g = group_find<kMmTile>(offsets, groups, M, s, row);
-        m0 = g.m0;
-        n0 = col * kMmTile;
-        row_end = g.end;
-        if (g.group >= groups) {
-            P = 0;   // no operand rows: the product is zero
-        } else {
-            rhs += (uint64_t)g.group * P * N * 4u;
-            rhs_scale += (uint64_t)g.group * (P / 8u) * N;
-        }
-    } else {
-        // P operand rows in all; group g's are offsets[g] / 4 .. The tiles of
-        // one group are spread over the XCDs (each gets consecutive ones), so
-        // that a large group's work is.
-        const uint32_t tiles_m = (M + kMmTile - 1) / kMmTile, per = tiles_m * tiles_n;
-        const uint32_t g = blockIdx.x / per;
-        const uint32_t t = xcd_tile(blockIdx.x - g * per, per);
-        const uint32_t walk = t / (kMmGroupRows * tiles_n);
-        const uint32_t first_row = walk * kMmGroupRows;
-        const uint32_t rows = min((uint32_t)kMmGroupRows, tiles_m - first_row);
-        const uint32_t in_walk = t - walk * kMmGroupRows * tiles_n;
-        m0 = (first_row + in_walk % rows) * kMmTile;
-        n0 = in_walk / rows * kMmTile;
-        row_end = M;
-        uint32_t a, b;
-        group_bounds(offsets, groups, 4u * P, g, a, b);
-        a = __builtin_amdgcn_readfirstlane(a / 32u);   // whole blocks
-        b = __builtin_amdgcn_readfirstlane(b / 32u);
-        lhs += (uint64_t)a * 8u * 4u * M;
-        lhs_scale += (uint64_t)a * M;
-        rhs += (uint64_t)a * 8u * 4u * N;
-        rhs_scale += (uint64_t)a * N;
-        P = (b - a) * 8u;
-        out = (uint8_t *)out + (uint64_t)g * M * N * ES;
-    }
-
+    GroupedJob job = {lhs, lhs_scale, rhs, rhs_scale, (uint8_t *)out, P, 0, 0, 0, false};
+    if (!grouped_job<MODE, kMmTile, kMmTile, kMmGroupRows, ES>(job, offsets, groups, M, N, tiles_n, lane))
+        return;
     MmSource src;
-    mm_source(src, grp ? rhs : lhs, grp ? rhs_scale : lhs_scale, grp ? N : M, grp ? n0 : m0);
+    mm_source(src, grp ? job.rhs : job.lhs, grp ? job.rhs_scale : job.lhs_scale, grp ? N : M, grp ? job.n0 : job.m0);
     f32x16_t acc[2][4];
-    mm_tile_product<F>(acc, lds, src, P, 1u, grp, wq, lane);
-
-    grouped_results<F, EPI>(acc, lhs, lhs_scale, rhs, rhs_scale, P, M, N, m0 + 64u * wq, n0 + 128u * grp, row_end,
-                            lane & 31u, lane >> 5, out);
+    mm_tile_product<F>(acc, lds, src, job.P, 1u, grp, wq, lane);
+    grouped_results<F, EPI>(acc, job, M, N, job.m0 + 64u * wq, job.n0 + 128u * grp, lane & 31u, lane >> 5);
 }
 
 // ----------------------------------------------------------------------------
@@ -347,7 +399,7 @@ __device__ __forceinline__ void mid_copy(const MmSource &sa, const MmSource &sb,
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)dst, 4, vs, 0, 0, 0);
 }
 
-template <int FMT, int EPI>
+template <int FMT, int EPI, int MODE>
 __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
     const uint8_t *__restrict__ lhs, const uint8_t *__restrict__ lhs_scale, const uint8_t *__restrict__ rhs,
     const uint8_t *__restrict__ rhs_scale, const int32_t *__restrict__ offsets, uint32_t groups, uint32_t P,
@@ -355,26 +407,19 @@ __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
 {
     __shared__ __attribute__((aligned(16))) uint8_t lds[kMmStages * kMidStageBytes + kMmSpareBytes];
     constexpr int F = MfmaFmt<FMT>::value;
+    constexpr uint32_t ES = EPI == kEpiF32 ? 4 : 2;
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t wm = 64u * (wave & 1u), wn = 128u * (wave >> 1);
     const uint32_t i = lane & 31u, h = lane >> 5;
 
-    const GroupScan sc = group_scan<kMidRows>(offsets, groups, M, lane);
-    uint32_t row, col;
-    if (!grouped_tile<2 * kMmGroupRows>(sc, tiles_n, row, col))
+    GroupedJob job = {lhs, lhs_scale, rhs, rhs_scale, (uint8_t *)out, P, 0, 0, 0, false};
+    if (!grouped_job<MODE, kMidRows, kMmTile, 2 * kMmGroupRows, ES>(job, offsets, groups, M, N, tiles_n, lane))
         return;
-    const GroupTile g = group_find<kMidRows>(offsets, groups, M, sc, row);
-    const uint32_t n0 = col * kMmTile;
-    if (g.group >= groups) {
-        P = 0;
-    } else {
-        rhs += (uint64_t)g.group * P * N * 4u;
-        rhs_scale += (uint64_t)g.group * (P / 8u) * N;
-    }
+    P = job.P;
     MmSource sa, sb;
-    mm_source(sa, lhs, lhs_scale, M, g.m0);
-    mm_source(sb, rhs, rhs_scale, N, n0);
+    mm_source(sa, job.lhs, job.lhs_scale, M, job.m0);
+    mm_source(sb, job.rhs, job.rhs_scale, N, job.n0);
     uint8_t *spare = lds + kMmStages * kMidStageBytes;
 
     f32x16_t acc[2][4];
@@ -442,7 +487,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
     }
     // no copy may land in the LDS of the workgroup that comes after this one
     __builtin_amdgcn_s_waitcnt(kWaitAllCopies);
-    grouped_results<F, EPI>(acc, lhs, lhs_scale, rhs, rhs_scale, P, M, N, g.m0 + wm, n0 + wn, g.end, i, h, out);
+    grouped_results<F, EPI>(acc, job, M, N, job.m0 + wm, job.n0 + wn, i, h);
 }
 
 // ----------------------------------------------------------------------------
@@ -582,7 +627,7 @@ __device__ __attribute__((noinline)) void stream_rare_part(const uint8_t *lhs, c
 #pragma unroll
     for (int r = 0; r < 16; r++) {
         const float v[4] = {acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
-        grouped_store<EPI, 4>(v, m0 + 8u * (r >> 2) + (r & 3), h, row_end, n0 + 4u * i, N, out);
+        grouped_store<EPI, 4, 0>(v, m0 + 8u * (r >> 2) + (r & 3), h, row_end, n0 + 4u * i, N, out);
     }
 }
 
@@ -601,21 +646,13 @@ __global__ __launch_bounds__(64 * CW * KW, 2) void grouped_stream_kernel(
     const uint32_t cw = wave % CW, kw = wave / CW;
     const uint32_t i = lane & 31u, h = lane >> 5;
 
-    const GroupScan sc = group_scan<kStreamRows>(offsets, groups, M, lane);
-    uint32_t row, col;
-    if (!grouped_tile<1>(sc, tiles_n, row, col))
+    GroupedJob job = {lhs, lhs_scale, rhs, rhs_scale, (uint8_t *)out, P, 0, 0, 0, false};
+    if (!rows_job<kStreamRows, CW * kStreamCols, 1, EPI == kEpiF32 ? 4 : 2>(job, offsets, groups, M, N, tiles_n, lane))
         return;
-    const GroupTile g = group_find<kStreamRows>(offsets, groups, M, sc, row);
-    const uint32_t n0 = (col * CW + cw) * kStreamCols;
-    if (g.group >= groups) {
-        P = 0;
-    } else {
-        rhs += (uint64_t)g.group * P * N * 4u;
-        rhs_scale += (uint64_t)g.group * (P / 8u) * N;
-    }
+    const uint32_t n0 = job.n0 + cw * kStreamCols;
     MmSource sa, sb;
-    mm_source(sa, lhs, lhs_scale, M, g.m0);
-    mm_source(sb, rhs, rhs_scale, N, n0);
+    mm_source(sa, job.lhs, job.lhs_scale, M, job.m0);
+    mm_source(sb, job.rhs, job.rhs_scale, N, n0);
     if (threadIdx.x < CW)
         rare[threadIdx.x] = 0;
 
@@ -630,7 +667,7 @@ __global__ __launch_bounds__(64 * CW * KW, 2) void grouped_stream_kernel(
     // A group of one row tile reads its weights once: past the caches, which
     // streams faster (64 experts x 32 rows, 4096 x 2048: 94 -> 87 us; with two row
     // tiles, where the second finds them in the cache: 57 us, 70 with the hint).
-    if (g.end - g.first <= kStreamRows)
+    if (job.one_tile)
         stream_steps<F, 1>(acc, sa, sb, P, s0, s1, i, h);
     else
         stream_steps<F, 0>(acc, sa, sb, P, s0, s1, i, h);
@@ -665,12 +702,17 @@ __global__ __launch_bounds__(64 * CW * KW, 2) void grouped_stream_kernel(
     __syncthreads();
     if (__builtin_amdgcn_readfirstlane(rare[cw]) != 0) {
         if (kw == 0)
-            stream_rare_part<F, EPI>(lhs, lhs_scale, rhs, rhs_scale, P, M, N, g.m0, n0, g.end, out);
+            stream_rare_part<F, EPI>(job.lhs, job.lhs_scale, job.rhs, job.rhs_scale, P, M, N, job.m0, n0, job.row_end,
+                                     job.out);
     } else {
+        const bool lines = whole_lines<EPI>(N);
 #pragma unroll
         for (uint32_t k = 0; k < RW; k++) {
-            const uint32_t r = kw * RW + k;
-            grouped_store<EPI, 4>(v[k], g.m0 + 8u * (r >> 2) + (r & 3u), h, g.end, n0 + 4u * i, N, out);
+            const uint32_t r = kw * RW + k, m = job.m0 + 8u * (r >> 2) + (r & 3u);
+            if (lines)
+                grouped_store<EPI, 4, 1>(v[k], m, h, job.row_end, n0 + 4u * i, N, job.out);
+            else
+                grouped_store<EPI, 4, 0>(v[k], m, h, job.row_end, n0 + 4u * i, N, job.out);
         }
     }
 }

@@ -98,7 +98,6 @@ def check_rows(sizes, tail, K, N, fmt, res, seed=0, patch=None, per_block=1):
     assert (got[offsets[-1]:] == 0).all(), "rows past the last group"
 
 
-# mean rows per group (rows / groups) pick the tile: 32 rows, 64 rows, 256 rows
 GROUPINGS = [([4], 0), ([32], 0), ([0, 0, 0], 32), ([4, 0, 36, 32], 12), ([32] * 9, 64), ([40, 8, 0, 100], 0),
              ([64, 64, 128], 0), ([100, 60, 92, 0, 128], 20), ([256], 0), ([260, 512, 4], 0), ([0, 700, 124], 36)]
 
@@ -129,7 +128,7 @@ def test_rows_many_groups():
 
 def test_rows_many_tiles():
     """Tiles past the walk of four tile rows and past the XCDs' shares."""
-    progress("grouped rows, 256-row tiles, 7 x 5 tiles")
+    progress("grouped rows, many tiles")
     check_rows([516, 0, 1028], 300, 96, 1160, "e5m2", torch.bfloat16)
     progress("grouped rows, 32-row tiles")
     check_rows([36] * 23, 100, 96, 516, "e4m3fn", torch.float32)
@@ -301,7 +300,7 @@ def test_other_stream_graph_and_repeats():
 # ---- each form of the product, by the rule that picks it -------------------------
 
 def test_two_column_waves():
-    """Few rows per group and enough tiles (rows / 32 times N / 256 from 384 on):
+    """Few rows per group and enough tiles (rows / 32 times N / 256 above 128):
     two waves side by side, the last of them past the last column."""
     g = np.random.default_rng(7)
     sizes = (32 * g.integers(0, 3, size=64)).tolist()
@@ -322,8 +321,7 @@ def test_two_column_waves():
 @pytest.mark.parametrize("sizes", [[128, 160, 132], [100, 256, 40, 300], [4, 500, 128]])
 @pytest.mark.parametrize("res", [torch.float32, torch.bfloat16])
 def test_middling_groups_rare_path(sizes, res):
-    """97 to 256 rows per group on average: 128-row tiles, with scale bytes of 255
-    and NaN codes in them."""
+    """Middling groups with scale bytes of 255 and NaN codes in them."""
     def scales(l, ls, r, rs):
         ls[1, 3:150] = 255
         rs[:, 1, :] = 20
@@ -334,7 +332,7 @@ def test_middling_groups_rare_path(sizes, res):
         l[3, 4 * 130 + 2] = 0x7F
         r[1, 2, 4 * 17 + 1] = 0xFF
 
-    progress("grouped rows, 128-row tiles %s %s" % (sizes, res))
+    progress("grouped rows, middling groups %s %s" % (sizes, res))
     check_rows(sizes, 20, 160, 300, "e4m3fn", res)
     check_rows(sizes, 20, 160, 300, "e4m3fn", res, patch=scales, per_block=4)
     check_rows(sizes, 20, 96, 132, "e4m3fn", res, patch=codes, per_block=4)
@@ -342,7 +340,7 @@ def test_middling_groups_rare_path(sizes, res):
 
 @pytest.mark.parametrize("mean", [140, 300])
 def test_many_groups_of_many_rows(mean):
-    """More groups than lanes of a wave, for the 128- and 256-row tiles."""
+    """More groups than lanes of a wave, of many rows."""
     g = np.random.default_rng(mean)
     sizes = (4 * g.integers(mean // 8, mean * 3 // 8, size=70)).tolist()
     sizes[3] = sizes[66] = 0
