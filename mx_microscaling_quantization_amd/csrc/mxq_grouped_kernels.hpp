@@ -263,7 +263,8 @@ __device__ __forceinline__ void grouped_store(const float *v, uint32_t m, uint32
 // Whether rows of N results start on 128-byte lines. Their stores then have the
 // non-temporal hint (weight gradients of 2048 x 4096: 277 -> 262 us); otherwise two
 // tiles write parts of one line, which the hint keeps the L2 from putting
-// together (38 groups of 3296 x 2132: 155 us, 236 with it).
+// together (38 groups of 3296 x 2132: 155 us, 236 with it). The lines' ends still cost
+// half as many requests again: 52 groups of 32 rows, 3680 x 1388, 156 us; x 1408, 102.
 template <int EPI> __device__ __forceinline__ bool whole_lines(uint32_t N)
 {
     return N % (EPI == kEpiF32 ? 32u : 64u) == 0;
@@ -325,7 +326,7 @@ __device__ __forceinline__ void grouped_results(const f32x16_t (&acc)[2][4], con
 }
 
 // ----------------------------------------------------------------------------
-// Many rows per group: the scaled matmul's 256 x 256 tile
+// Long contractions of many rows: the scaled matmul's 256 x 256 tile
 // ----------------------------------------------------------------------------
 
 template <int FMT, int EPI, int MODE>
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(kMmThreads) void grouped_matmul_kernel(
 }
 
 // ----------------------------------------------------------------------------
-// Middling rows per group: a 128 x 256 tile
+// Middling groups and short contractions: a 128 x 256 tile
 // ----------------------------------------------------------------------------
 //
 // Four waves of 64 x 128, one per SIMD; two workgroups share a CU (registers
@@ -362,6 +363,9 @@ __global__ __launch_bounds__(kMmThreads) void grouped_matmul_kernel(
 // one barrier per K step, the copies of step s + 2 issued when step s is read.
 // Per K step the workgroup copies 16 operand rows of 256 containers (rhs) and of
 // 128 (lhs, two rows per load), and 2 scale rows of each: 7 loads per wave.
+// LDS bounds it: per step a CU's 8 waves read 96 KiB and 48 KiB are copied in, some
+// 1150 cycles at 128 bytes each, for 1024 of the matrix cores; the 256 x 256 tile
+// copies 32 KiB (32768 x 4096 by 4096 x 4096: 530 us, that one 496).
 constexpr int kMidThreads = 256;
 constexpr uint32_t kMidRows = 128;
 constexpr uint32_t kMidQuadA = kMidRows * 16 + 128;   // an lhs row quad, padded
@@ -491,7 +495,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
 }
 
 // ----------------------------------------------------------------------------
-// Few rows per group: the weights stream through registers
+// Few rows per group, or few tiles: the weights stream through registers
 // ----------------------------------------------------------------------------
 //
 // With few rows a product is bound by reading its expert's weights once. A
