@@ -91,8 +91,11 @@ int mxq_grouped_matmul(const void *lhs, const void *lhs_scale, const void *rhs, 
     // contraction and the number of tiles (a weight of 4096 x 4096 or
     // 2048 x 2048 e4m3fn, 268 MB of them, us):
     //   rows per group      32-row tiles  128-row tiles  256-row tiles
-    //   64                      57           62-71           79
-    //   128                    90-92         60-74          76-81
+    //   48                      64             67             -
+    //   64                      58            56-67          79
+    //   80                      79             67             -
+    //   96                     78-91          57-70           -
+    //   128                    90-92          61-72          76-81
     //   350 (4096 x 4096)        -           124             127
     //   414 (4096 x 2048)        -            68              65
     //   2048 (4096 x 4096)       -           547             500
@@ -108,7 +111,7 @@ int mxq_grouped_matmul(const void *lhs, const void *lhs_scale, const void *rhs, 
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     int64_t tiles_n = up(N, mxq::kMmTile);
     int kind = 0;
-    if (mean <= 96 || 2 * up(rows, mxq::kMidRows) * tiles_n <= kCus)
+    if (mean <= 64 || 2 * up(rows, mxq::kMidRows) * tiles_n <= kCus)
         kind = 3;
     else if (mean <= 384 || P <= 256)
         kind = 2;

@@ -377,12 +377,19 @@ constexpr int kMidCopies = 7;
 // Copies of K step `step` by wave w: rhs row quad w; lhs row pairs 2 w and
 // 2 w + 1; one scale load (waves 0 and 1: rhs row w; wave 2: both lhs rows;
 // wave 3: an empty one, so that every wave has the same count).
+template <int NT>
 __device__ __forceinline__ void mid_copy(const MmSource &sa, const MmSource &sb, uint8_t *stage, uint8_t *spare,
                                          uint32_t P, uint32_t step, uint32_t w, uint32_t lane)
 {
-    mm_copy_quad(sb, stage + kMidB, P, step, w, lane);
     const bool in = step * kMmStepRows < P;
     const uint32_t nrows = in ? min(P - step * kMmStepRows, kMmStepRows) : 0u;
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(sb.data + (in ? (uint64_t)step * kMmStepRows * sb.pitch : 0ull)), (short)0,
+        in ? (int)(nrows * sb.pitch - sb.col_bytes) : 0, kMmBufferFlags);
+#pragma unroll
+    for (uint32_t v = 0; v < 4; v++)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t *)(stage + kMidB + kMmQuadPitch * w + 1024u * v), 16,
+                                                 16u * lane, (4u * w + v) * sb.pitch, 0, NT ? kBufferNT : 0);
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
         (void *)(sa.data + (in ? (uint64_t)step * kMmStepRows * sa.pitch : 0ull)), (short)0,
         in ? (int)(nrows * sa.pitch - sa.col_bytes) : 0, kMmBufferFlags);
@@ -403,30 +410,13 @@ __device__ __forceinline__ void mid_copy(const MmSource &sa, const MmSource &sb,
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)dst, 4, vs, 0, 0, 0);
 }
 
-template <int FMT, int EPI, int MODE>
-__global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
-    const uint8_t *__restrict__ lhs, const uint8_t *__restrict__ lhs_scale, const uint8_t *__restrict__ rhs,
-    const uint8_t *__restrict__ rhs_scale, const int32_t *__restrict__ offsets, uint32_t groups, uint32_t P,
-    uint32_t M, uint32_t N, uint32_t tiles_n, void *__restrict__ out)
+// The product of one tile: this wave's 64 x 128 sums from row wm, column wn of it.
+template <int F, int NT>
+__device__ __forceinline__ void mid_steps(f32x16_t (&acc)[2][4], uint8_t *lds, const MmSource &sa, const MmSource &sb,
+                                          uint32_t P, uint32_t wm, uint32_t wn, uint32_t wave, uint32_t lane)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kMmStages * kMidStageBytes + kMmSpareBytes];
-    constexpr int F = MfmaFmt<FMT>::value;
-    constexpr uint32_t ES = EPI == kEpiF32 ? 4 : 2;
-    const uint32_t lane = threadIdx.x & 63u;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t wm = 64u * (wave & 1u), wn = 128u * (wave >> 1);
     const uint32_t i = lane & 31u, h = lane >> 5;
-
-    GroupedJob job = {lhs, lhs_scale, rhs, rhs_scale, (uint8_t *)out, P, 0, 0, 0, false};
-    if (!grouped_job<MODE, kMidRows, kMmTile, 2 * kMmGroupRows, ES>(job, offsets, groups, M, N, tiles_n, lane))
-        return;
-    P = job.P;
-    MmSource sa, sb;
-    mm_source(sa, job.lhs, job.lhs_scale, M, job.m0);
-    mm_source(sb, job.rhs, job.rhs_scale, N, job.n0);
     uint8_t *spare = lds + kMmStages * kMidStageBytes;
-
-    f32x16_t acc[2][4];
 #pragma unroll
     for (int a = 0; a < 2; a++)
 #pragma unroll
@@ -437,7 +427,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
     const uint32_t nsteps = (P + kMmStepRows - 1) / kMmStepRows;
 #pragma unroll
     for (uint32_t st = 0; st < 2; st++)
-        mid_copy(sa, sb, lds + st * kMidStageBytes, spare, P, st, wave, lane);
+        mid_copy<NT>(sa, sb, lds + st * kMidStageBytes, spare, P, st, wave, lane);
     uint32_t cur_i = 0;
     for (uint32_t s = 0; s < nsteps; s++) {
         const uint32_t fre_i = cur_i == 0 ? kMmStages - 1 : cur_i - 1u;   // step s - 1's stage
@@ -463,7 +453,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
         r.as[0] = st[a_sc];
         r.as[1] = st[a_sc + 1];
         r.bs = *reinterpret_cast<const uint32_t *>(st + b_sc);
-        mid_copy(sa, sb, lds + fre_i * kMidStageBytes, spare, P, s + 2, wave, lane);
+        mid_copy<NT>(sa, sb, lds + fre_i * kMidStageBytes, spare, P, s + 2, wave, lane);
         __builtin_amdgcn_s_waitcnt(mm_wait_vm_lgkm(63));   // my reads
         __builtin_amdgcn_sched_barrier(0);
         i32x8_t aop[2], bop[4];
@@ -491,7 +481,36 @@ __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
     }
     // no copy may land in the LDS of the workgroup that comes after this one
     __builtin_amdgcn_s_waitcnt(kWaitAllCopies);
-    grouped_results<F, EPI>(acc, job, M, N, job.m0 + wm, job.n0 + wn, i, h);
+}
+
+template <int FMT, int EPI, int MODE>
+__global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
+    const uint8_t *__restrict__ lhs, const uint8_t *__restrict__ lhs_scale, const uint8_t *__restrict__ rhs,
+    const uint8_t *__restrict__ rhs_scale, const int32_t *__restrict__ offsets, uint32_t groups, uint32_t P,
+    uint32_t M, uint32_t N, uint32_t tiles_n, void *__restrict__ out)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kMmStages * kMidStageBytes + kMmSpareBytes];
+    constexpr int F = MfmaFmt<FMT>::value;
+    constexpr uint32_t ES = EPI == kEpiF32 ? 4 : 2;
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t wm = 64u * (wave & 1u), wn = 128u * (wave >> 1);
+
+    GroupedJob job = {lhs, lhs_scale, rhs, rhs_scale, (uint8_t *)out, P, 0, 0, 0, false};
+    if (!grouped_job<MODE, kMidRows, kMmTile, 2 * kMmGroupRows, ES>(job, offsets, groups, M, N, tiles_n, lane))
+        return;
+    MmSource sa, sb;
+    mm_source(sa, job.lhs, job.lhs_scale, M, job.m0);
+    mm_source(sb, job.rhs, job.rhs_scale, N, job.n0);
+    f32x16_t acc[2][4];
+    // a group of one row tile reads its weights once, past the caches (128 experts x
+    // 128 rows, 4096 x 1536: 181 -> 168 us; with two row tiles, 256 rows: 96 us, 114
+    // with the hint)
+    if (MODE == kGroupRows && job.one_tile)
+        mid_steps<F, 1>(acc, lds, sa, sb, job.P, wm, wn, wave, lane);
+    else
+        mid_steps<F, 0>(acc, lds, sa, sb, job.P, wm, wn, wave, lane);
+    grouped_results<F, EPI>(acc, job, M, N, job.m0 + wm, job.n0 + wn, lane & 31u, lane >> 5);
 }
 
 // ----------------------------------------------------------------------------

@@ -2,8 +2,9 @@
 contraction and the rows per group pick another form, and of what is cleared
 without a product. Bounds as in test_gpu_grouped.
 
-rows:  128 x 256 tiles on fewer than half of the CUs: 32-row tiles; else up to 384
-       rows per group or 1024 values: 128-row tiles; else 256-row tiles
+rows:  128 x 256 tiles on up to half of the CUs, or up to 64 rows per group: 32-row
+       tiles; else up to 384 rows per group or 1024 values: 128-row tiles;
+       else 256-row tiles
 wgrad: fewer than 768 rows of the contraction per group: 128-row tiles, else 256
 """
 import numpy as np
@@ -137,3 +138,17 @@ def test_wgrad_empty_groups(M, N, res):
     progress("grouped wgrad, empty groups, M=%d N=%d" % (M, N))
     check_wgrad([0, 32, 0, 0, 64, 0], M, N, "e4m3fn", res, seed=M)
     check_wgrad([0, 1568, 0], M, N, "e4m3fn", res, seed=N)
+
+
+@pytest.mark.parametrize("patch", [None, scales])
+@pytest.mark.parametrize("res", [torch.float32, torch.bfloat16])
+def test_groups_of_one_and_of_several_128_row_tiles(res, patch):
+    """Weights past the caches where a group is one tile; 64 rows on average (32-row
+    tiles) and more (128-row ones)."""
+    g = np.random.default_rng(12)
+    for mean in (64, 68):
+        sizes = (4 * g.integers(0, mean // 2, size=40)).tolist()
+        sizes[5], sizes[9], sizes[20] = 128, 132, 0
+        tail = 40 * mean - sum(sizes) if sum(sizes) < 40 * mean else 4
+        progress("grouped rows, 40 groups of %d rows at most, %d rows in all" % (max(sizes), sum(sizes) + tail))
+        check_rows(sizes, tail, 96, 2600, "e4m3fn", res, seed=mean, patch=patch, per_block=4)
