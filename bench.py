@@ -98,8 +98,8 @@ KERNEL_SOURCES = {
     "quantize": [_CSRC + f for f in ("mxq_quantize_kernels.hpp", "mxq_quantize_api.hip", "mxq_host.hpp")],
     "dequantize": [_CSRC + f for f in ("mxq_quantize_kernels.hpp", "mxq_dequantize_kernels.hpp",
                                        "mxq_dequantize_api.hip", "mxq_host.hpp")],
-    "matmul": [_CSRC + f for f in ("mxq_quantize_kernels.hpp", "mxq_matmul_kernels.hpp", "mxq_matmul_api.hip",
-                                   "mxq_host.hpp")],
+    "matmul": [_CSRC + f for f in ("mxq_quantize_kernels.hpp", "mxq_matmul_ranges.hpp", "mxq_matmul_kernels.hpp",
+                                   "mxq_matmul_api.hip", "mxq_host.hpp")],
     "quantize_axis": [_CSRC + f for f in ("mxq_quantize_kernels.hpp", "mxq_axis_kernels.hpp", "mxq_axis_api.hip",
                                           "mxq_host.hpp")],
 }

@@ -302,6 +302,10 @@ template <int F, int EPI>
 __device__ __forceinline__ void grouped_results(const f32x16_t (&acc)[2][4], const GroupedJob &job, uint32_t M,
                                                 uint32_t N, uint32_t wm0, uint32_t wn0, uint32_t i, uint32_t h)
 {
+    // a part past the group's rows or the columns has nothing to store, and its
+    // sums times a NaN are no reason for the rare path
+    if (wm0 >= job.row_end || wn0 >= N)
+        return;
     // 0 times a finite sum is a zero, of anything else a NaN that stays: one
     // instruction per sum, in eight chains (a class test per sum and the scalar
     // logic to collect them took 0.7 us more per tile)

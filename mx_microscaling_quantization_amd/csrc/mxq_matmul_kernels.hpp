@@ -22,6 +22,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mxq_matmul_ranges.hpp"
 #include "mxq_quantize_kernels.hpp"
 
 namespace mxq {
@@ -304,12 +305,13 @@ __device__ __forceinline__ void mm_step_255(f32x16_t (&acc)[4], const i32x8_t &a
 }
 
 // A buffer over the K step `step` of an operand from column c0 (as the
-// copies use): rows past P and bytes past the operand read as zero.
+// copies use): rows past P and bytes past the operand read as zero; empty
+// where c0 is past the operand's last column.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mm_step_rsrc(const MmSource &s, uint32_t P, uint32_t step)
 {
     const uint32_t rows_left = min(P - step * kMmStepRows, kMmStepRows);
     return __builtin_amdgcn_make_buffer_rsrc((void *)(s.data + (uint64_t)step * kMmStepRows * s.pitch), (short)0,
-                                             (int)(rows_left * s.pitch - s.col_bytes), kMmBufferFlags);
+                                             (int)operand_range(rows_left, s.C, s.col_bytes / 4u), kMmBufferFlags);
 }
 
 // The rare path: a wave's whole 64 x 128 part of the tile computed again,
@@ -357,12 +359,13 @@ __device__ __forceinline__ void mm_tile_255(f32x16_t (&acc)[2][4], const uint8_t
             uint32_t as = 0x7Fu, bs = 0x7F7F7F7Fu;
             if (g < groups) {
                 // the scale row from column c0 on, as the copies read it:
-                // containers past the operand's last read as zero
+                // containers past the operand's last read as zero, all of
+                // them where c0 is past it itself
                 const uint64_t srow = dense ? g : (g & 3u) + 32u * (g >> 2);
                 const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
-                    (void *)(sa.scale + srow * M), (short)0, (int)sa.scale_cols, kMmBufferFlags);
+                    (void *)(sa.scale + srow * M), (short)0, (int)scale_range(1u, M, c0a), kMmBufferFlags);
                 const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
-                    (void *)(sb.scale + srow * N), (short)0, (int)sb.scale_cols, kMmBufferFlags);
+                    (void *)(sb.scale + srow * N), (short)0, (int)scale_range(1u, N, c0b), kMmBufferFlags);
                 as = __builtin_amdgcn_raw_buffer_load_b8(rsa, 2u * i + a, 0, 0);
                 bs = __builtin_amdgcn_raw_buffer_load_b32(rsb, 4u * i, 0, 0);
             }
@@ -557,6 +560,12 @@ __global__ __launch_bounds__(kMmThreads) void scaled_matmul_kernel(
     mm_source(src, grp ? rhs : lhs, grp ? rhs_scale : lhs_scale, grp ? N : M, grp ? n0 : m0);
     f32x16_t acc[2][4];
     mm_tile_product<F>(acc, lds, src, P, dense, grp, wq, lane);
+
+    // A part past the result's last row or column has nothing to store, and its
+    // sums (zeros, or of bytes next to the operands' last columns) times a NaN
+    // are no reason for the rare path.
+    if (m0 + wm >= M || n0 + wn >= N)
+        return;
 
     // The matrix cores read a scale byte of 255 as NaN, where it stands for
     // 2^128. A sum that is not finite may come from one, so the wave then
