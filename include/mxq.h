@@ -456,7 +456,8 @@ size_t mxq_clip_grad_norm_workspace_bytes(const int64_t *elements, const int *el
  *     out    = round(g * factor)
  * The squares are added in 64 bits; the factor and the norm that is returned
  * are rounded to fp32 (a norm beyond its range is returned as infinity; the
- * factor is still that of the 64-bit norm). An infinity or NaN among the
+ * factor is still that of the 64-bit norm, and one below fp32's normal numbers
+ * is applied in 64 bits). An infinity or NaN among the
  * elements leaves the values as they are; the norm tells.
  *
  *   grads, outs  host arrays of `count` device pointers, each aligned to its

@@ -124,7 +124,8 @@ template <int DT> __device__ __forceinline__ double clip_squares(const ClipPart 
     return s0 + s1;
 }
 
-template <int DT> __device__ __forceinline__ void clip_store(const ClipPart &part, float factor)
+// F: float, or double for a factor below fp32's normal numbers.
+template <int DT, typename F> __device__ __forceinline__ void clip_store(const ClipPart &part, F factor)
 {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t V = Elem<DT>::vec, S = sizeof(T);
@@ -135,10 +136,20 @@ template <int DT> __device__ __forceinline__ void clip_store(const ClipPart &par
         elems_to_f32<DT>(__builtin_bit_cast(ElemVec<DT>, part.v[i]), f);
 #pragma unroll
         for (uint32_t k = 0; k < V; k++)
-            f[k] *= factor;
+            f[k] = (float)(f[k] * factor);
         const uint64_t n = part.left > skip ? (part.left - skip) / S : 0;
         store_elems<DT, 1>((T *)(part.out + skip), n < V ? (uint32_t)n : V, f);
     }
+}
+
+template <typename F> __device__ __forceinline__ void clip_store_as(const ClipPart &part, F factor)
+{
+    if (part.type == kElemBF16)
+        clip_store<kElemBF16>(part, factor);
+    else if (part.type == kElemF16)
+        clip_store<kElemF16>(part, factor);
+    else
+        clip_store<kElemF32>(part, factor);
 }
 
 // The workgroup's sum of `v`, in a fixed order, in every thread.
@@ -214,7 +225,12 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipTable tabl
     const bool clip = norm > max_norm && norm < __builtin_inf();
     if (in_place && !clip)
         return;
-    const float factor = clip ? (float)(max_norm / norm) : 1.0f;
+    // the factor is rounded to fp32 but where that would leave it fewer bits (a norm
+    // of 1e41, which only the 64-bit sum holds, clipped to 1): products in 64 bits,
+    // rounded once, then
+    const double exact = clip ? max_norm / norm : 1.0;
+    const float factor = (float)exact;
+    const bool tiny = exact < 0x1p-126;
     const uint32_t tiles = table.first_tile[table.tensors];
     uint32_t back = blockIdx.x;   // tiles from the end
     if (back >= tiles)
@@ -223,12 +239,10 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipTable tabl
     for (; back < tiles; back += gridDim.x) {
         ClipPart part;
         clip_load<1>(clip_place(table, tiles - 1 - back, n, part), part);
-        if (part.type == kElemBF16)
-            clip_store<kElemBF16>(part, factor);
-        else if (part.type == kElemF16)
-            clip_store<kElemF16>(part, factor);
+        if (tiny)
+            clip_store_as(part, exact);
         else
-            clip_store<kElemF32>(part, factor);
+            clip_store_as(part, factor);
     }
 }
 
