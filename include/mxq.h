@@ -398,7 +398,8 @@ int mxq_moe_combine(const void *y, int64_t rows, int64_t N, int elem_dtype, cons
  *     grad_weights[t][j] = sum over n of grad[t][n] * y[dest[t][j]][n] (fp32),
  *                          0 for a pair without a row
  * grad [tokens, N], y and grad_y [rows, N] of elem_dtype; src and dest of one
- * mxq_moe_sort. All pointers 16-byte aligned; every element written.
+ * mxq_moe_sort. (Where a caller has changed one of them, a pair has a row if
+ * dest names a row whose src names the pair: the others' grad_weights are 0.) All pointers 16-byte aligned; every element written.
  */
 int mxq_moe_combine_backward(const void *grad, const void *y, int64_t rows, int64_t N, int elem_dtype,
                              const int32_t *src, const int32_t *dest, const float *weights, int64_t tokens,

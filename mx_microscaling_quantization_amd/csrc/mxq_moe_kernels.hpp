@@ -449,7 +449,9 @@ __global__ __launch_bounds__(256) void combine_kernel(const typename Elem<DT>::t
 // gradient rows are read once per slot, all but the first time from the caches.
 // (Token by token, with the gradient row read once and `slots` rows of y and
 // grad_y open at a time, 6007 x 8 rows of 2052 bf16 took 161 us.)
-// Workgroups past the rows' own clear grad_w of the pairs without a row.
+// Workgroups past the rows' own clear grad_w of the pairs without a row: of each
+// pair exactly one of the two, the one row that dest and src both name or these,
+// writes it.
 // A lane has KV vectors of each row in flight, all of them where the row has
 // up to 8 per lane. y and grad_y go past the caches (rows of 4096 bf16, 16384 x 4:
 // 226 us, 254 without the hint).
@@ -525,7 +527,9 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
 #pragma unroll
     for (int d = LANES / 2; d > 0; d >>= 1)
         acc += __shfl_xor(acc, d);
-    if (lane == 0)
+    // (src and dest may disagree: a pair that the caller took out of dest alone is a
+    // pair without a row, whose zero the other workgroups write)
+    if (lane == 0 && (uint32_t)dest[pair] == r)
         grad_w[pair] = acc;
 }
 
