@@ -408,8 +408,9 @@ int mxq_moe_combine_backward(const void *grad, const void *y, int64_t rows, int6
 /*
  * mxq_grouped_matmul -- the experts' products:
  *     out[r][n] = sum over k < 4P of L[k][r] * R_g[k][n] for r in group g,
- * zeros for the rows past the last group. Operand layout, element values and
- * accumulation as for mxq_scaled_matmul, with dense scales.
+ * zeros for the rows of no group (past the last one, and before the first where
+ * offsets[0] > 0). Operand layout, element values and accumulation as for
+ * mxq_scaled_matmul, with dense scales.
  *
  *   lhs, lhs_scale  P x 4*rows FP8 data and [P/8, rows] scales: the sorted
  *                   rows, quantized along K (mxq_moe_gather_quantize or
@@ -419,6 +420,8 @@ int mxq_moe_combine_backward(const void *grad, const void *y, int64_t rows, int6
  *                   for the gradient of the input, the weights [N', K'] with
  *                   dim -1 (P = K'/4, N = N').
  *   offsets         int32 [groups + 1] on the device; entries multiples of 4.
+ *                   A part of a plan's offsets (some of its experts) will do, if
+ *                   it starts at a multiple of 4 entries, or as a copy.
  *   groups          1 .. MXQ_MOE_MAX_EXPERTS.
  *   P               multiple of 8 (0: a zero result); rows and N multiples of
  *                   4, up to MXQ_MATMUL_MAX_COLS.

@@ -635,7 +635,8 @@ def grouped_scaled_matmul(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs: torch
                           offsets: torch.Tensor, fmt: str = "e4m3fn", res_dtype: torch.dtype = torch.bfloat16,
                           out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """The experts' products: out[r] = X[r] @ W_g for the sorted rows r of
-    group g, zeros for the rows past the last group.
+    group g, zeros for the rows of no group (past the last one; before the first
+    where ``offsets[0]`` is above 0).
 
     ``lhs`` [P, 4 rows] with dense scales [P/8, rows] are the sorted rows
     quantized along K = 4P (:func:`moe_gather_quantize`, or

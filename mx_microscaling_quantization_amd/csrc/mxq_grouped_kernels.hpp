@@ -8,7 +8,7 @@
 // point with about 13 fraction bits below the largest of them. With group g
 // the columns offsets[g] .. offsets[g + 1] - 1:
 //   rows:   out[r][n]    = sum over k of L[k][r] * R_g[k][n] for r in group g,
-//           zero for the rows past the last group
+//           zero for the rows of no group (before the first one, past the last)
 //   wgrad:  out[g][m][n] = sum over k in group g of L[k][m] * R[k][n]
 //           (the sorted rows are the contraction: groups of whole MX blocks)
 //
@@ -48,7 +48,8 @@ __device__ __forceinline__ void group_bounds(const int32_t *offsets, uint32_t gr
 // scan over the lanes gives each lane's first tile and the number of tiles.
 struct GroupScan {
     uint32_t per, first;    // groups per lane; this lane's first row tile
-    uint32_t real, total;   // row tiles of the groups; with those past the last group
+    uint32_t real;          // row tiles of the groups
+    uint32_t total;         // the same with those past the last group
 };
 
 template <uint32_t TILE>
@@ -142,22 +143,28 @@ struct GroupedJob {
 
 // Rows: the groups' tiles (TILE rows x COLS columns) are walked in sets of WALK
 // tile rows column by column, so that the workgroups an XCD runs at a time share
-// operand panels. The rows past the last group are cleared by further workgroups,
+// operand panels. The rows of no group, past the last one or before the first (the
+// offsets of some experts of a plan), are cleared by further workgroups,
 // which are not part of the XCDs' even shares (64 experts, 62 of them used, x 32
 // rows, 4096 x 2048: with them some XCDs got 70 products for their 64 places, 101
-// us instead of 81). False: this workgroup has no product.
+// us instead of 81). The launch has at least one tile row of them. False: this
+// workgroup has no product.
 template <uint32_t TILE, uint32_t COLS, uint32_t WALK, uint32_t ES>
 __device__ __forceinline__ bool rows_job(GroupedJob &job, const int32_t *offsets, uint32_t groups, uint32_t M,
                                          uint32_t N, uint32_t tiles_n, uint32_t lane)
 {
     const GroupScan s = group_scan<TILE>(offsets, groups, M, lane);
-    const uint32_t real = s.real * tiles_n, all = s.total * tiles_n;
+    const uint32_t real = s.real * tiles_n;
     const uint32_t t = xcd_tile(blockIdx.x, real);
     if (t >= real) {
-        if (t < all) {
-            uint32_t a, b;
-            group_bounds(offsets, groups, M, groups, a, b);
-            zero_share(job.out + (uint64_t)a * N * ES, (uint64_t)(b - a) * N * ES, t - real, all - real);
+        uint32_t a, b;
+        group_bounds(offsets, groups, M, groups, a, b);
+        const uint32_t before = min((uint32_t)max(offsets[0], 0), M);
+        const uint32_t tiles = s.total - s.real + (before + TILE - 1) / TILE;
+        const uint32_t n = min(tiles * tiles_n, gridDim.x - real);
+        if (t - real < n) {
+            zero_share(job.out + (uint64_t)a * N * ES, (uint64_t)(b - a) * N * ES, t - real, n);
+            zero_share(job.out, (uint64_t)before * N * ES, t - real, n);
         }
         return false;
     }
