@@ -441,6 +441,12 @@ def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tenso
         return torch.empty(*shape, dtype=dtype, device=device)
 
 
+# Tells autograd that a kernel has written to the caller's tensors (one, or a
+# list), so that a backward pass that kept one of them from before raises, as
+# after torch's own in-place operations.
+_written = torch.autograd.graph.increment_version
+
+
 def _check_tensor(name: str, t: torch.Tensor, shape, dtypes, device: torch.device | None = None) -> None:
     """A contiguous device tensor of this shape (an int: of that many
     dimensions) and one of these types, on ``device`` if given."""
@@ -587,13 +593,16 @@ def moe_combine(y: torch.Tensor, plan: MoEPlan, weights: torch.Tensor | None = N
         raise ValueError("y has %d rows, the plan %d" % (n, rows))
     if weights is not None:
         _check_tensor("weights", weights, (T, k), _FLOAT32, dev)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _new((T, N), y.dtype, dev, stream)
     else:
         _check_tensor("out", out, (T, N), (y.dtype,), dev)
     _check(_call_on(dev, lib.mxq_moe_combine, y.data_ptr(), rows, N, code, plan.dest.data_ptr(),
                     None if weights is None else weights.data_ptr(), T, k, out.data_ptr(),
                     _stream_handle(stream, dev)))
+    if given:
+        _written(out)
     return out
 
 
@@ -617,6 +626,7 @@ def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, plan: MoEPlan, wei
         raise ValueError("y has %d rows, the plan %d" % (n, rows))
     _check_tensor("grad", grad, (T, N), (y.dtype,), dev)
     _check_tensor("weights", weights, (T, k), _FLOAT32, dev)
+    given = [t for t in (grad_y, grad_weights) if t is not None]
     if grad_y is None:
         grad_y = _new((rows, N), y.dtype, dev, stream)
     else:
@@ -628,6 +638,8 @@ def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, plan: MoEPlan, wei
     _check(_call_on(dev, lib.mxq_moe_combine_backward, grad.data_ptr(), y.data_ptr(), rows, N, code,
                     plan.src.data_ptr(), plan.dest.data_ptr(), weights.data_ptr(), T, k, grad_y.data_ptr(),
                     grad_weights.data_ptr(), _stream_handle(stream, dev)))
+    if given:
+        _written(given)
     return grad_y, grad_weights
 
 
@@ -662,13 +674,16 @@ def grouped_scaled_matmul(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs: torch
     _check_tensor("lhs_scale", lhs_scale, (P // 8, M), _UINT8, dev)
     _check_tensor("rhs_scale", rhs_scale, (G, P // 8, N), _UINT8, dev)
     _check_tensor("offsets", offsets, (G + 1,), _INT32, dev)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _new((M, N), res_dtype, dev, stream)
     else:
         _check_tensor("out", out, (M, N), (res_dtype,), dev)
     _check(_call_on(dev, lib.mxq_grouped_matmul, lhs.data_ptr(), lhs_scale.data_ptr(), rhs.data_ptr(),
                     rhs_scale.data_ptr(), offsets.data_ptr(), G, P, M, N, code, RES_DTYPES[res_dtype], out.data_ptr(),
                     _stream_handle(stream, dev)))
+    if given:
+        _written(out)
     return out
 
 
@@ -692,13 +707,16 @@ def grouped_scaled_matmul_wgrad(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs:
     dev = lhs.device
     _check_tensor("offsets", offsets, 1, _INT32, dev)
     G = offsets.shape[0] - 1
-    if out is None:
+    given = out is not None
+    if not given:
         out = _new((max(G, 0), M, N), res_dtype, dev, stream)
     else:
         _check_tensor("out", out, (G, M, N), (res_dtype,), dev)
     _check(_call_on(dev, lib.mxq_grouped_matmul_wgrad, lhs.data_ptr(), lhs_scale.data_ptr(), rhs.data_ptr(),
                     rhs_scale.data_ptr(), offsets.data_ptr(), G, P, M, N, code, RES_DTYPES[res_dtype], out.data_ptr(),
                     _stream_handle(stream, dev)))
+    if given:
+        _written(out)
     return out
 
 
@@ -748,6 +766,8 @@ def _norm_call(grads, max_norm, outs, stream):
     ws = _new((lib.mxq_clip_grad_norm_workspace_bytes(np_, cp, n),), torch.uint8, dev, stream)
     _check(_call_on(dev, lib.mxq_clip_grad_norm, pp, op, np_, cp, n, max_norm, norm.data_ptr(), ws.data_ptr(),
                     _stream_handle(stream, dev)))
+    if outs is not None:
+        _written(outs)
     return norm
 
 
