@@ -466,7 +466,9 @@ size_t mxq_clip_grad_norm_workspace_bytes(const int64_t *elements, const int *el
  *
  *   grads, outs  host arrays of `count` device pointers, each aligned to its
  *                element; outs NULL: the norm only. outs[i] == grads[i] scales
- *                in place; otherwise they do not overlap.
+ *                in place; otherwise outs[i] overlaps no gradient, and no two of
+ *                outs overlap in any case (a tensor scaled twice would be read
+ *                before or after the other's write).
  *   elements     host array, elements per tensor (0 allowed), each tensor
  *                contiguous.
  *   elem_dtypes  host array of enum mxq_elem_dtype.

@@ -758,6 +758,12 @@ def _norm_call(grads, max_norm, outs, stream):
         if ocodes != codes or onumels != numels:
             raise ValueError("out must hold a tensor of each gradient's size and type")
     n = len(grads)
+    # the workgroups of a tensor listed twice would each scale what the others have
+    # scaled or not (a tensor without elements has no address of its own)
+    if optrs is not None and len(set(optrs)) != n:
+        some = [p for p, e in zip(optrs, numels) if e]
+        if len(set(some)) != len(some):
+            raise ValueError("the tensors that are scaled must not share memory")
     pa, pp = _c_array("Q", ptrs)
     oa, op = (None, None) if optrs is None else (pa, pp) if optrs is ptrs else _c_array("Q", optrs)
     na, np_ = _c_array("q", numels)
@@ -783,7 +789,8 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream: torch.cuda.Stream |
     float32 device scalar).
 
     The tensors (bf16, f16 or f32, mixed) are scaled in place, or into the
-    tensors of ``out``. A norm that is not finite leaves the values as they
+    tensors of ``out``; those must not share memory with each other (one
+    gradient of several layers is listed once). A norm that is not finite leaves the values as they
     are. Nothing is copied to the host.
     """
     if not max_norm >= 0.0:
