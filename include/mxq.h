@@ -5,8 +5,9 @@
  * library allocates nothing, keeps no state between calls and is safe to call
  * from several host threads at once. Every call is asynchronous on the
  * caller's HIP stream: it validates its arguments on the host, enqueues its
- * kernel (the sort of a long list and the clipping: two or more) and returns. Faults during execution surface at the caller's next
- * synchronisation, not here.
+ * kernel (the sort of a long list and the clipping: two or more) and returns.
+ * Faults during execution surface at the caller's next synchronisation, not
+ * here.
  *
  * What the quantize computes (the pages "MX Microscaling: Quantize,
  * Block-Scaling and E8M0" -- the numerics -- and "MX-FP8 Microscaling

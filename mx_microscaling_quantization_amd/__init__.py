@@ -421,6 +421,12 @@ def quantize_axis(x: torch.Tensor, out_dtype: str = "e4m3fn", dim: int = -1, dat
 # ---------------------------------------------------------------------------
 # Mixture of experts
 # ---------------------------------------------------------------------------
+#
+# The calls take no part in autograd: a result never requires a gradient, also
+# where an argument does. Gradients are calls of their own (moe_combine_backward,
+# the grouped product with the weights' dim -1 form, the _wgrad product and, for
+# the gather, moe_combine without weights), for a torch.autograd.Function or by
+# hand.
 
 class MoEPlan(NamedTuple):
     """Where each (token, slot) pair goes when a batch is sorted by expert
@@ -614,7 +620,9 @@ def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, plan: MoEPlan, wei
 
     grad_y [rows, N] (y's type) is zero in the rows without a pair,
     grad_weights [tokens, slots] (float32) for the pairs without a row. (The
-    gradient of the unweighted combine is the gather.)
+    gradient of the unweighted combine is the gather of its rows;
+    :func:`moe_gather_quantize` gives it quantized, as the products before it
+    read it. There is no call that gathers without quantizing.)
     """
     lib = load()
     code = _elem_code(y.dtype)

@@ -88,25 +88,31 @@ int mxq_grouped_matmul(const void *lhs, const void *lhs_scale, const void *rhs, 
     if (rc != MXQ_OK || rows == 0 || N == 0)
         return rc;
     // The tile follows from the mean rows per group, the length of the
-    // contraction and the number of tiles (a weight of 4096 x 4096 or
-    // 2048 x 2048 e4m3fn, 268 MB of them, us):
-    //   rows per group      32-row tiles  128-row tiles  256-row tiles
-    //   48                      64             67             -
-    //   64                      58            56-67          79
-    //   80                      79             67             -
-    //   96                     78-91          57-70           -
-    //   128                    90-92          61-72          76-81
-    //   350 (4096 x 4096)        -           124             127
-    //   414 (4096 x 2048)        -            68              65
-    //   2048 (4096 x 4096)       -           547             500
+    // contraction and the number of tiles (268 MB of e4m3fn weights, 2048 x 2048 and
+    // 4096 x 4096 up to 128 rows, 4096 x 4096 and 4096 x 2048 from there on; groups of
+    // one size; us, all forms in turn):
+    //   rows per group  32-row tiles  128-row tiles  256-row tiles
+    //   32                 46-48          59-66          72-82
+    //   64                 58-59          59-67          74-84
+    //   80                   79             68             -
+    //   96                 80-92          59-70          75-86
+    //   128                  94           59-71          78-85
+    //   256                   -             87             71
+    //   352                   -          130-132        125-126
+    //   512                   -          148-149        131-132
+    //   2048 (4096 x 4096)    -            545            495
+    // With sizes of 0.6 to 1.4 times the mean, more of the tiles are parts of one: 352
+    // rows 135-137 and 121, 2048 rows 573 and 538. (The border of 384 is from groups of
+    // about 350 rows at which the two forms took 124 and 127; in this table the 256-row
+    // tiles lead from 256 rows on.)
     // A short contraction is mostly the stores of its results, which several
     // smaller workgroups on a CU overlap with other tiles' products (16 experts,
-    // 32768 rows, 4096 columns: 64 values 63 us, 256-row tiles 73; 512 values
-    // 121 and 128; 1024 values equal; 2048 values 297 and 285).
+    // 32768 rows, 4096 columns: 64 values 65 us, 256-row tiles 72; 512 values
+    // 113 and 116; 1024 values 166 and 168; 2048 values 301 and 275).
     // Where 128-row tiles do not fill half of the CUs, the time is one tile's
     // whole contraction, which the small ones share out among their waves
-    // (512 x 4096 by 4096 x 4096: 24 us and 46; with 182 such tiles, 1536 rows
-    // over 2048 values by 3584 columns: 32 and 28).
+    // (512 x 4096 by 4096 x 4096: 25 us and 46; with 168 such tiles, 1536 rows
+    // over 2048 values by 3584 columns: 30 and 27).
     const int64_t mean = rows / groups, kCus = 256;
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     int64_t tiles_n = up(N, mxq::kMmTile);
@@ -116,8 +122,8 @@ int mxq_grouped_matmul(const void *lhs, const void *lhs_scale, const void *rhs, 
     else if (mean <= 384 || P <= 256)
         kind = 2;
     // with fewer small tiles than that, narrower ones whose four waves all share
-    // the contraction (8 experts x 32 rows, 4096 x 4096, 128 tiles: 24 us, wide
-    // ones 32; 2 x 64 rows, 4096 x 8192, 160 tiles: 31 and 28)
+    // the contraction (32 rows per expert, 4096 x 4096: 8 experts, 128 tiles, 25 us,
+    // wide ones 33; 10 experts, 160 tiles, 40 and 34)
     if (kind == 3 && 2 * up(rows, mxq::kStreamRows) * tiles_n <= kCus) {
         kind = 4;
         tiles_n = up(N, mxq::kStreamCols);
@@ -141,10 +147,11 @@ int mxq_grouped_matmul_wgrad(const void *lhs, const void *lhs_scale, const void 
         return rc;
     // With little to multiply per group the time is that of writing the result,
     // which several smaller workgroups on a CU overlap with the products of
-    // others (weight gradients of 2048 x 2048, 271 rows of the contraction per
-    // group: 78 us, 256-row tiles 84; 39 of 1920 x 768, 512 rows: 58 and 63;
-    // 35 of 672 x 3328, 1067 rows: 132 and 129; 16 of 2048 x 4096, 2064 rows:
-    // 293 and 276).
+    // others (32 weight gradients of 2048 x 2048, 288 rows of the contraction per
+    // group: 79 us, 256-row tiles 91; 39 of 1920 x 768, 512 rows: 54 and 64;
+    // 35 of 672 x 3328, 1056 rows: 117 and 123, of sizes of 0.6 to 1.4 times that 117
+    // and 114; 16 of 2048 x 4096, 768 rows: 130 and 136, uneven 134 and 132, 2048 rows:
+    // 276 and 258).
     const bool mid = 4 * P / groups < 768;
     const int64_t tile = mid ? mxq::kMidRows : mxq::kMmTile;
     const uint32_t threads = mid ? mxq::kMidThreads : mxq::kMmThreads;

@@ -376,7 +376,7 @@ __global__ __launch_bounds__(kMmThreads) void grouped_matmul_kernel(
 // 128 (lhs, two rows per load), and 2 scale rows of each: 7 loads per wave.
 // LDS bounds it: per step a CU's 8 waves read 96 KiB and 48 KiB are copied in, some
 // 1150 cycles at 128 bytes each, for 1024 of the matrix cores; the 256 x 256 tile
-// copies 32 KiB (32768 x 4096 by 4096 x 4096: 530 us, that one 496).
+// copies 32 KiB (16 groups of 2048 rows, 4096 x 4096: 545 us, that one 495).
 constexpr int kMidThreads = 256;
 constexpr uint32_t kMidRows = 128;
 constexpr uint32_t kMidQuadA = kMidRows * 16 + 128;   // an lhs row quad, padded
@@ -515,8 +515,8 @@ __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(
     mm_source(sb, job.rhs, job.rhs_scale, N, job.n0);
     f32x16_t acc[2][4];
     // a group of one row tile reads its weights once, past the caches (128 experts x
-    // 128 rows, 4096 x 1536: 181 -> 168 us; with two row tiles, 256 rows: 96 us, 114
-    // with the hint)
+    // 128 rows, 4096 x 1536: 182 -> 172 us; with two row tiles, 64 experts x 256 rows of
+    // 2048 x 2048: 97 us, 117 with the hint)
     if (MODE == kGroupRows && job.one_tile)
         mid_steps<F, 1>(acc, lds, sa, sb, job.P, wm, wn, wave, lane);
     else
@@ -699,8 +699,9 @@ __global__ __launch_bounds__(64 * CW * KW, 2) void grouped_stream_kernel(
     const uint32_t per = (nsteps + KW - 1) / KW;
     const uint32_t s0 = min(kw * per, nsteps), s1 = min(s0 + per, nsteps);
     // A group of one row tile reads its weights once: past the caches, which
-    // streams faster (64 experts x 32 rows, 4096 x 2048: 94 -> 87 us; with two row
-    // tiles, where the second finds them in the cache: 57 us, 70 with the hint).
+    // streams faster (64 experts x 32 rows, 4096 x 2048: 93 -> 87 us; with two row
+    // tiles, 64 rows of 2048 x 2048, where the second finds them in the cache: 57 us, 69
+    // with the hint).
     if (job.one_tile)
         stream_steps<F, 1>(acc, sa, sb, P, s0, s1, i, h);
     else

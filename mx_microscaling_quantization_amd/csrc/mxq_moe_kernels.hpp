@@ -452,9 +452,11 @@ __global__ __launch_bounds__(256) void combine_kernel(const typename Elem<DT>::t
 // Workgroups past the rows' own clear grad_w of the pairs without a row: of each
 // pair exactly one of the two, the one row that dest and src both name or these,
 // writes it.
-// A lane has KV vectors of each row in flight, all of them where the row has
-// up to 8 per lane. y and grad_y go past the caches (rows of 4096 bf16, 16384 x 4:
-// 226 us, 254 without the hint).
+// A lane has KV vectors of each row in flight: one where the row has up to 64, else
+// two at a time. y and grad_y go past the caches (rows of 4096 bf16, 16384 x 4:
+// 226 us, 254 without the hint). The stores keep the hint also where rows are not
+// whole lines (ordinary stores: 6007 x 8 rows of 2052 97 us, 94 with it; 16384 x 4 rows
+// of 4100 270 and 251).
 template <int DT, uint32_t LANES, uint32_t KV>
 __global__ __launch_bounds__(256) void combine_backward_kernel(
     const typename Elem<DT>::type *__restrict__ grad, const typename Elem<DT>::type *__restrict__ y, uint32_t rows,
@@ -673,8 +675,8 @@ __global__ __launch_bounds__(64 * kAlongWaves) void gather_quantize_along_kernel
 // all 32 of them in scalar registers before the lanes past the tensor leave.
 // RUNS: tiles are numbered run of columns by run of columns and every XCD takes
 // consecutive ones, so that a token's 512 bytes of a run come from that XCD's
-// L2 for all slots but the first (8192 x 8 rows of 4096 bf16: 93 -> 64 us); else
-// band by band, which writes in order (16384 x 1 rows of 8192: 75 us against 80).
+// L2 for all slots but the first (8192 x 8 rows of 4096 bf16: 89 -> 61 us); else
+// band by band, which writes in order (16384 x 1 rows of 8192: 61 us in either order).
 template <int IN, int OUT, int NB, int RUNS>
 __global__ __launch_bounds__(64) void gather_quantize_down_kernel(const uint16_t *__restrict__ x,
                                                                   const int32_t *__restrict__ src, uint32_t rows,
