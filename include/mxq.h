@@ -450,6 +450,44 @@ int mxq_grouped_matmul_wgrad(const void *lhs, const void *lhs_scale, const void 
                              const int32_t *offsets, int64_t groups, int64_t P, int64_t M, int64_t N, int fmt,
                              int res_dtype, void *out, void *stream);
 
+/*
+ * mxq_scaled_matmul_fp4 -- block-scaled matmul with e2m1 weights.
+ *
+ *     out[m][n] = sum over k < 4P of L[k][m] * R[k][n]
+ * with operand layouts, element values, scale bytes (255 included) and
+ * accumulation as for mxq_scaled_matmul, R in e2m1 and L in any of the three
+ * formats. e2m1 operands are what mxq_quantize and mxq_quantize_axis write: rows of
+ * 16-bit containers.
+ *
+ *   lhs, lhs_scale  the activations, quantized along K (mxq_quantize_axis, dim
+ *                   -1): P rows of M containers (4M bytes in FP8, 2M in e2m1) and
+ *                   their scale image (P x M) or dense scales [P/8, M].
+ *   rhs, rhs_scale  the weights [K, N] quantized with dim -2 to e2m1: P x 2N bytes
+ *                   and their scales (P x N, or dense [P/8, N]).
+ *   P               multiple of 8; P == 0 gives a zero result.
+ *   M               any length, one row included; multiples of 4 are faster from
+ *                   some hundred rows on.
+ *   N               multiple of 4. M, N <= MXQ_MATMUL_MAX_COLS.
+ *   lhs_fmt         enum mxq_out_dtype.
+ *   res_dtype       enum mxq_res_dtype.
+ *   flags           MXQ_FLAG_DENSE_SCALE: both scales are dense.
+ *   out             M x N results, row-major.
+ * All pointers 16-byte aligned. Returns MXQ_OK once enqueued, else an MXQ_E_*
+ * code with nothing enqueued.
+ */
+int mxq_scaled_matmul_fp4(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs_scale, int64_t P,
+                          int64_t M, int64_t N, int lhs_fmt, int res_dtype, unsigned flags, void *out, void *stream);
+
+/*
+ * mxq_grouped_matmul_fp4 -- mxq_grouped_matmul with the experts' weights in
+ * e2m1: rhs is [groups, P, 2N] bytes with dense scales [groups, P/8, N], lhs the
+ * sorted rows in any of the three formats. Groups, offsets and rows of no group as
+ * there.
+ */
+int mxq_grouped_matmul_fp4(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs_scale,
+                           const int32_t *offsets, int64_t groups, int64_t P, int64_t rows, int64_t N, int lhs_fmt,
+                           int res_dtype, void *out, void *stream);
+
 /* Workspace of mxq_clip_grad_norm; 0 for invalid arguments. The three arrays
  * are host memory. */
 size_t mxq_clip_grad_norm_workspace_bytes(const int64_t *elements, const int *elem_dtypes, int64_t count);

@@ -21,7 +21,8 @@ import torch  # loaded first so that the library binds to torch's HIP runtime
 __all__ = [
     "IN_DTYPES", "OUT_DTYPES", "RES_DTYPES", "ELEM_DTYPES", "MXQError", "quantize", "dequantize", "quantize_axis",
     "scaled_matmul", "scaled_matmul_quantize", "MoEPlan", "moe_rows", "moe_sort", "moe_gather_quantize", "moe_combine",
-    "moe_combine_backward", "grouped_scaled_matmul", "grouped_scaled_matmul_wgrad", "clip_grad_norm", "grad_norm",
+    "moe_combine_backward", "grouped_scaled_matmul", "grouped_scaled_matmul_wgrad", "scaled_matmul_fp4", "grouped_scaled_matmul_fp4",
+    "clip_grad_norm", "grad_norm",
     "data_bytes", "scale_image_bytes", "result_bytes", "data_shape", "scale_image_shape",
     "axis_view_shape", "logical_scale_view", "status_string", "library_path", "load",
 ]
@@ -113,6 +114,10 @@ def load():
             fn = getattr(lib, name)
             fn.argtypes = [p, p, p, p, p, i64, i64, i64, i64, c.c_int, c.c_int, p, p]
             fn.restype = c.c_int
+        lib.mxq_scaled_matmul_fp4.argtypes = [p, p, p, p, i64, i64, i64, c.c_int, c.c_int, c.c_uint, p, p]
+        lib.mxq_scaled_matmul_fp4.restype = c.c_int
+        lib.mxq_grouped_matmul_fp4.argtypes = [p, p, p, p, p, i64, i64, i64, i64, c.c_int, c.c_int, p, p]
+        lib.mxq_grouped_matmul_fp4.restype = c.c_int
         lib.mxq_clip_grad_norm_workspace_bytes.argtypes = [p, p, i64]
         lib.mxq_clip_grad_norm_workspace_bytes.restype = c.c_size_t
         lib.mxq_clip_grad_norm.argtypes = [p, p, p, p, i64, c.c_double, p, p, p]
@@ -721,6 +726,94 @@ def grouped_scaled_matmul_wgrad(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs:
     else:
         _check_tensor("out", out, (G, M, N), (res_dtype,), dev)
     _check(_call_on(dev, lib.mxq_grouped_matmul_wgrad, lhs.data_ptr(), lhs_scale.data_ptr(), rhs.data_ptr(),
+                    rhs_scale.data_ptr(), offsets.data_ptr(), G, P, M, N, code, RES_DTYPES[res_dtype], out.data_ptr(),
+                    _stream_handle(stream, dev)))
+    if given:
+        _written(out)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Products with 4-bit weights
+# ---------------------------------------------------------------------------
+
+# Bytes of a container (four codes).
+_CONTAINER = {"e4m3fn": 4, "e5m2": 4, "e2m1": 2}
+
+
+def _fp4_result(lhs, lhs_fmt, res_dtype):
+    """(format code, rows) of the activations of a product with 4-bit weights."""
+    code = _out_code(lhs_fmt)
+    if res_dtype not in RES_DTYPES:
+        raise MXQError(10, "result type must be float32 or bfloat16, got %s" % res_dtype)
+    _check_tensor("lhs", lhs, 2, _UINT8)
+    P, width = lhs.shape
+    if P % 8 or width % _CONTAINER[lhs_fmt]:
+        raise ValueError("lhs must be [P, %d M] with P a multiple of 8 in format %s" % (_CONTAINER[lhs_fmt], lhs_fmt))
+    return code, width // _CONTAINER[lhs_fmt]
+
+
+def scaled_matmul_fp4(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs: torch.Tensor, rhs_scale: torch.Tensor,
+                      lhs_fmt: str = "e4m3fn", res_dtype: torch.dtype = torch.bfloat16,
+                      out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None,
+                      dense_scale: bool = False) -> torch.Tensor:
+    """Block-scaled matmul with e2m1 weights: X @ W for activations X [M, K] quantized
+    with ``dim=-1`` to ``lhs_fmt`` (any of the three formats) and weights W [K, N]
+    quantized with ``dim=-2`` to ``"e2m1"`` (:func:`quantize_axis`).
+
+    ``lhs`` is [P, 4M] (e2m1: [P, 2M]) and ``rhs`` [P, 2N] with K = 4P; their scales are
+    images [P, M] and [P, N], or dense [P/8, M] and [P/8, N] with ``dense_scale``. M is
+    any number of rows, N a multiple of 4. Returns [M, N] float32 or bfloat16;
+    arithmetic as in :func:`scaled_matmul`.
+    """
+    lib = load()
+    code, M = _fp4_result(lhs, lhs_fmt, res_dtype)
+    dev, P = lhs.device, lhs.shape[0]
+    _check_tensor("rhs", rhs, 2, _UINT8, dev)
+    P2, N2 = rhs.shape
+    if P2 != P or N2 % 8:
+        raise ValueError("rhs must be [P, 2 N] with lhs's P = %d and N a multiple of 4" % P)
+    N = N2 // 2
+    rows = P // 8 if dense_scale else P
+    _check_tensor("lhs_scale", lhs_scale, (rows, M), _UINT8, dev)
+    _check_tensor("rhs_scale", rhs_scale, (rows, N), _UINT8, dev)
+    given = out is not None
+    if not given:
+        out = _new((M, N), res_dtype, dev, stream)
+    else:
+        _check_tensor("out", out, (M, N), (res_dtype,), dev)
+    _check(_call_on(dev, lib.mxq_scaled_matmul_fp4, lhs.data_ptr(), lhs_scale.data_ptr(), rhs.data_ptr(),
+                    rhs_scale.data_ptr(), P, M, N, code, RES_DTYPES[res_dtype],
+                    FLAG_DENSE_SCALE if dense_scale else 0, out.data_ptr(), _stream_handle(stream, dev)))
+    if given:
+        _written(out)
+    return out
+
+
+def grouped_scaled_matmul_fp4(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs: torch.Tensor, rhs_scale: torch.Tensor,
+                              offsets: torch.Tensor, lhs_fmt: str = "e4m3fn",
+                              res_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                              stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """:func:`grouped_scaled_matmul` with the experts' weights in e2m1: ``rhs``
+    [groups, P, 2N] with dense scales [groups, P/8, N], the sorted rows in
+    ``lhs_fmt`` (any of the three formats)."""
+    lib = load()
+    code, M = _fp4_result(lhs, lhs_fmt, res_dtype)
+    dev, P = lhs.device, lhs.shape[0]
+    _check_tensor("rhs", rhs, 3, _UINT8, dev)
+    G, P2, N2 = rhs.shape
+    if P2 != P or N2 % 8:
+        raise ValueError("rhs must be [groups, P, 2 N] with lhs's P = %d and N a multiple of 4" % P)
+    N = N2 // 2
+    _check_tensor("lhs_scale", lhs_scale, (P // 8, M), _UINT8, dev)
+    _check_tensor("rhs_scale", rhs_scale, (G, P // 8, N), _UINT8, dev)
+    _check_tensor("offsets", offsets, (G + 1,), _INT32, dev)
+    given = out is not None
+    if not given:
+        out = _new((M, N), res_dtype, dev, stream)
+    else:
+        _check_tensor("out", out, (M, N), (res_dtype,), dev)
+    _check(_call_on(dev, lib.mxq_grouped_matmul_fp4, lhs.data_ptr(), lhs_scale.data_ptr(), rhs.data_ptr(),
                     rhs_scale.data_ptr(), offsets.data_ptr(), G, P, M, N, code, RES_DTYPES[res_dtype], out.data_ptr(),
                     _stream_handle(stream, dev)))
     if given:

@@ -148,8 +148,8 @@ struct GroupedJob {
 // which are not part of the XCDs' even shares (64 experts, 62 of them used, x 32
 // rows, 4096 x 2048: with them some XCDs got 70 products for their 64 places, 101
 // us instead of 81). The launch has at least one tile row of them. False: this
-// workgroup has no product.
-template <uint32_t TILE, uint32_t COLS, uint32_t WALK, uint32_t ES>
+// workgroup has no product. RC: bytes of a container of the weights.
+template <uint32_t TILE, uint32_t COLS, uint32_t WALK, uint32_t ES, uint32_t RC = 4>
 __device__ __forceinline__ bool rows_job(GroupedJob &job, const int32_t *offsets, uint32_t groups, uint32_t M,
                                          uint32_t N, uint32_t tiles_n, uint32_t lane)
 {
@@ -177,7 +177,7 @@ __device__ __forceinline__ bool rows_job(GroupedJob &job, const int32_t *offsets
     job.n0 = col * COLS;
     job.row_end = g.end;
     job.one_tile = g.end - g.first <= TILE;
-    job.rhs += (uint64_t)g.group * job.P * N * 4u;
+    job.rhs += (uint64_t)g.group * job.P * N * RC;
     job.rhs_scale += (uint64_t)g.group * (job.P / 8u) * N;
     return true;
 }

@@ -1,0 +1,226 @@
+"""GPU tests of the products with 4-bit weights against exact (64-bit) sums of the
+quantized operands. Bounds as in test_gpu_grouped: the matrix cores add a block's
+products in fixed point with about 13 fraction bits below the largest, blocks in fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mx_microscaling_quantization_amd as mxq
+import oracle
+from conftest import progress
+from test_gpu_grouped import compare, dev, host, quantized
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = ["e2m1", "e4m3fn", "e5m2"]
+
+
+def values(codes, scale, fmt):
+    """[K, C] float64 of codes [P, C containers] and dense scales [P/8, C]."""
+    P, C = codes.shape[0], scale.shape[1]
+    if fmt == "e2m1":   # nibbles from the lowest on: elements 2, 3, 0, 1
+        word = np.ascontiguousarray(codes).view("<u2").reshape(P, C)
+        codes = np.stack([(word >> s) & 15 for s in (8, 12, 0, 4)], -1).astype(np.uint8)
+    v = oracle.decode(codes, fmt).reshape(P, C, 4).transpose(0, 2, 1).reshape(4 * P, C)
+    return v * np.ldexp(1.0, np.repeat(scale.astype(np.int64), 32, axis=0) - 127)
+
+
+def image_of(dense):
+    """The scale image that holds these dense scales, 0xEE in its other rows."""
+    G, C = dense.shape
+    image = np.full((8 * G, C), 0xEE, np.uint8)
+    for i in range(G):
+        image[(i % 4) + 32 * (i // 4)] = dense[i]
+    return image
+
+
+def check(M, K, N, fmt, res=torch.float32, patch=None, per_block=1, image=False, seed=0):
+    progress("fp4 product %d x %d x %d, %s to %s" % (M, K, N, fmt, res))
+    l, ls = quantized(M, K, -1, fmt, seed + M + K)
+    r, rs = quantized(K, N, -2, "e2m1", seed + N)
+    if patch:
+        patch(l, ls, r, rs)
+    # results behind the last row stay as they were
+    room = torch.full((M * N + 64,), 7.0, dtype=res, device="cuda")
+    scales = (image_of(ls), image_of(rs)) if image else (ls, rs)
+    mxq.scaled_matmul_fp4(dev(l), dev(scales[0]), dev(r), dev(scales[1]), fmt, res, out=room[:M * N].view(M, N),
+                          dense_scale=not image)
+    got = host(room)
+    assert (got[M * N:] == 7).all()
+    compare(got[:M * N].reshape(M, N), values(l, ls, fmt), values(r, rs, "e2m1"), res, per_block)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 31, 32, 33, 64, 65, 100])
+def test_few_rows(M, fmt):
+    check(M, 160, 132, fmt)
+    check(M, 32, 4, fmt, torch.bfloat16)
+    check(M, 1056, 260, fmt, torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("res", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K,N", [(100, 64, 8448), (97, 96, 8452), (600, 160, 1284), (604, 96, 3844), (1027, 192, 2052),
+                                   (2048, 224, 2048), (1500, 1056, 2060), (772, 1184, 2820)])
+def test_many_rows(M, K, N, fmt, res):
+    """Every form of the product: wide 32-row tiles, 128- and 256-row tiles, whole and in
+    parts, contractions that end inside a stage, row counts that are no multiple of 4."""
+    check(M, K, N, fmt, res)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K,N", [(3, 160, 36), (90, 96, 132), (600, 288, 1284), (800, 1120, 2820)])
+def test_scale_image(M, K, N, fmt):
+    check(M, K, N, fmt, torch.bfloat16, image=True)
+
+
+def scale_255(l, ls, r, rs):
+    ls[1, ::3] = 255
+    ls[1, 1::3] = 100
+    rs[1, ::2] = 255
+    rs[1, 1::2] = 20
+    rs[0, -1] = 255
+    ls[0, :] = 10
+
+
+def scale_255_left(l, ls, r, rs):
+    ls[-1, -2:] = 255
+    rs[-1, :] = 20
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("patch", [scale_255, scale_255_left])
+@pytest.mark.parametrize("M,K,N", [(5, 96, 68), (70, 64, 8200), (600, 160, 1284), (1028, 1088, 2052)])
+def test_scale_255(M, K, N, patch, fmt):
+    """A scale byte of 255 stands for 2^128, on either side."""
+    check(M, K, N, fmt, torch.float32, patch, per_block=4)
+
+
+@pytest.mark.parametrize("M,K,N", [(5, 96, 68), (70, 64, 8200), (600, 160, 1284), (1028, 1088, 2052)])
+def test_nan_codes_stay_in_their_row(M, K, N):
+    def patch(l, ls, r, rs):
+        l[3, 4 * (M - 2) + 1] = 0x7F
+
+    check(M, K, N, "e4m3fn", torch.float32, patch, per_block=4)
+
+
+def test_no_contraction_is_zero():
+    empty = [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in ((0, 20), (0, 5), (0, 16), (0, 8))]
+    out = torch.full((5, 8), 3.0, device="cuda")
+    mxq.scaled_matmul_fp4(*empty, "e4m3fn", torch.float32, out=out, dense_scale=True)
+    assert int(torch.count_nonzero(out)) == 0
+    assert mxq.scaled_matmul_fp4(empty[0][:, :0], empty[1][:, :0], *empty[2:], "e4m3fn").shape == (0, 8)
+
+
+def test_quantized_by_the_library():
+    """Operands as quantize_axis writes them, with scale images: the product of what they
+    decode to; nothing else is between the calls."""
+    g = torch.Generator().manual_seed(3)
+    x, w = torch.randn((70, 192), generator=g).to(torch.bfloat16), torch.randn((192, 260), generator=g).to(torch.bfloat16)
+    for fmt in FORMATS:
+        l, ls = mxq.quantize_axis(x.cuda(), fmt, -1)
+        r, rs = mxq.quantize_axis(w.cuda(), "e2m1", -2)
+        got = host(mxq.scaled_matmul_fp4(l, ls, r, rs, fmt, torch.float32))
+        rows = [(i % 4) + 32 * (i // 4) for i in range(6)]
+        L = values(l.cpu().numpy(), ls.cpu().numpy()[rows], fmt)
+        compare(got, L, values(r.cpu().numpy(), rs.cpu().numpy()[rows], "e2m1"), torch.float32)
+
+
+# ---- groups -------------------------------------------------------------------------
+
+def check_rows(sizes, tail, K, N, fmt, res, first=0, patch=None, per_block=1):
+    offsets = (first + np.concatenate([[0], np.cumsum(sizes)])).astype(np.int32)
+    rows, G = int(offsets[-1]) + tail, len(sizes)
+    progress("fp4 groups %s after %d, tail %d, %d x %d, %s to %s" % (sizes[:12], first, tail, K, N, fmt, res))
+    l, ls = quantized(rows, K, -1, fmt, rows + K)
+    r, rs = (np.stack(t) for t in zip(*[quantized(K, N, -2, "e2m1", 77 * (g % 9) + N) for g in range(G)]))
+    if patch:
+        patch(l, ls, r, rs)
+    room = torch.full((rows * N + 64,), 7.0, dtype=res, device="cuda")
+    mxq.grouped_scaled_matmul_fp4(dev(l), dev(ls), dev(r), dev(rs), dev(offsets), fmt, res,
+                                  out=room[:rows * N].view(rows, N))
+    got = host(room)
+    assert (got[rows * N:] == 7).all()
+    got = got[:rows * N].reshape(rows, N)
+    assert (got[:first] == 0).all() and (got[offsets[-1]:] == 0).all()
+    L = values(l, ls, fmt)
+    for g in range(G):
+        a, b = offsets[g], offsets[g + 1]
+        if a != b:
+            compare(got[a:b], L[:, a:b], values(r[g], rs[g], "e2m1"), res, per_block)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("sizes,first,tail,K,N", [([4], 0, 0, 32, 4), ([0, 0, 0], 0, 32, 64, 36), ([4, 0, 36, 32], 64, 12, 160, 132),
+                                                  ([32] * 70, 0, 64, 96, 1544), ([128, 160, 0, 132], 0, 20, 160, 2600),
+                                                  ([516, 0, 1028], 4, 300, 1088, 1160), ([700, 132, 68, 260], 32, 0, 96, 516)])
+def test_groups(sizes, first, tail, K, N, fmt):
+    check_rows(sizes, tail, K, N, fmt, torch.bfloat16, first)
+
+
+@pytest.mark.parametrize("sizes,K,N", [([32, 64], 160, 132), ([128, 160, 132], 160, 2600), ([516, 1028], 1088, 1160)])
+def test_groups_scale_255(sizes, K, N):
+    def patch(l, ls, r, rs):
+        ls[1, 3:40] = 255
+        rs[:, 1, :] = 20
+        rs[-1, 0, ::7] = 255
+        ls[0, :] = 12
+
+    for fmt in FORMATS:
+        check_rows(sizes, 8, K, N, fmt, torch.float32, patch=patch, per_block=4)
+
+
+def test_groups_out_of_range_are_clamped():
+    K, N, rows = 64, 64, 128
+    l, ls = map(dev, quantized(rows, K, -1, "e4m3fn", 1))
+    r, rs = (dev(np.stack(t)) for t in zip(*[quantized(K, N, -2, "e2m1", g) for g in range(4)]))
+    want = mxq.grouped_scaled_matmul_fp4(l, ls, r, rs, dev(np.array([0, 32, 64, 96, 128], np.int32)))
+    for off in ([0, 32, 64, 4096, 2 ** 31 - 4], [-64, 32, 16, 64, 96], [2 ** 31 - 4] * 5, [-4] * 5):
+        out = mxq.grouped_scaled_matmul_fp4(l, ls, r, rs, dev(np.array(off, np.int32)))
+        torch.cuda.synchronize()
+        if off[0] <= 0 and off[1] == 32:    # rows 0 .. 15 are only group 0's in both lists
+            assert torch.equal(out[:16], want[:16])
+
+
+def test_other_stream_graph_and_repeats():
+    off = dev(np.array([0, 32, 128, 128, 192], np.int32))
+    l, ls = map(dev, quantized(192, 128, -1, "e4m3fn", 1))
+    r, rs = (dev(np.stack(t)) for t in zip(*[quantized(128, 132, -2, "e2m1", g) for g in range(4)]))
+    big = [dev(t) for t in (*quantized(1028, 1088, -1, "e2m1", 2), *quantized(1088, 1160, -2, "e2m1", 3))]
+
+    def run(**kw):
+        return (mxq.grouped_scaled_matmul_fp4(l, ls, r, rs, off, **kw),
+                mxq.scaled_matmul_fp4(*big, "e2m1", dense_scale=True, **kw),
+                mxq.scaled_matmul_fp4(l, ls, r[0], rs[0], "e4m3fn", dense_scale=True, **kw))
+
+    want = run()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        got = run(stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run()
+    for _ in range(4):
+        for t in got:
+            t.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        _ = (got[0].float() * 2).sum().item()
+
+
+def test_results_given_by_the_caller_count_a_version():
+    l, ls = map(dev, quantized(8, 32, -1, "e4m3fn", 1))
+    r, rs = map(dev, quantized(32, 8, -2, "e2m1", 2))
+    out = torch.empty((8, 8), dtype=torch.bfloat16, device="cuda")
+    v = out._version
+    assert mxq.scaled_matmul_fp4(l, ls, r, rs, out=out, dense_scale=True) is out
+    mxq.grouped_scaled_matmul_fp4(l, ls, r[None], rs[None], dev(np.array([0, 8], np.int32)), out=out)
+    assert out._version == v + 2
