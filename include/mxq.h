@@ -82,11 +82,16 @@ enum mxq_status {
                           /* negative count of tensors or elements            */
     MXQ_E_ELEM_DTYPE = 14, /* element type is not BF16, F16 or F32 (ids: not  */
                           /* 4 or 8 bytes)                                    */
-    MXQ_E_VALUE = 15      /* max_norm is negative or NaN                      */
+    MXQ_E_VALUE = 15,     /* max_norm is negative or NaN                      */
+    MXQ_E_ACT = 16        /* activation is not SILU or SWIGLU                 */
 };
 
 /* Element types of the calls that take plain tensors. */
 enum mxq_elem_dtype { MXQ_ELEM_BF16 = 0, MXQ_ELEM_F16 = 1, MXQ_ELEM_F32 = 2 };
+
+/* Activations between the two products of a layer: silu(z) = z / (1 + e^-z) of F
+ * columns, or silu(z[0 .. F - 1]) * z[F .. 2F - 1] of 2 F. */
+enum mxq_act { MXQ_ACT_SILU = 0, MXQ_ACT_SWIGLU = 1 };
 
 /* Result types of mxq_dequantize. */
 enum mxq_res_dtype { MXQ_RES_F32 = 0, MXQ_RES_BF16 = 1 };
@@ -487,6 +492,47 @@ int mxq_scaled_matmul_fp4(const void *lhs, const void *lhs_scale, const void *rh
 int mxq_grouped_matmul_fp4(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs_scale,
                            const int32_t *offsets, int64_t groups, int64_t P, int64_t rows, int64_t N, int lhs_fmt,
                            int res_dtype, void *out, void *stream);
+
+/* Pairs of a mxq_moe_few_tokens call. */
+#define MXQ_MOE_FEW_PAIRS 1024
+
+/* Workspace of mxq_moe_few_tokens; 0 for invalid arguments. */
+size_t mxq_moe_few_tokens_workspace_bytes(int64_t tokens, int64_t slots, int64_t F, int64_t N);
+
+/*
+ * mxq_moe_few_tokens -- a whole mixture-of-experts layer for a few tokens:
+ *     out[t] = sum over j of weights[t][j] * (act(x[t] @ W1_e) @ W2_e),
+ *     e = ids[t][j]
+ * in two kernels without a sort, for decode steps. The activations are not
+ * quantized: weights are widened exactly, sums are fp32, what is between the
+ * products is kept to 16 bits or more of each value, and the sum over the slots is in
+ * slot order, rounded once. Scale bytes as for mxq_scaled_matmul, 255 included.
+ *
+ *   x          device pointer, [tokens, K] of in_dtype (enum mxq_in_dtype).
+ *   ids        [tokens, slots] expert numbers of id_bytes (4 or 8) bytes; a number
+ *              outside 0 .. experts - 1 adds nothing, a token without any expert
+ *              gives zeros. An expert may be named twice.
+ *   weights    fp32 [tokens, slots].
+ *   slots, experts   as for mxq_moe_sort; tokens * slots <= MXQ_MOE_FEW_PAIRS.
+ *   w1, w1_scale   [experts, K/4, containers] data and dense [experts, K/32, ..]
+ *              scales of each expert's [K, F] (MXQ_ACT_SILU) or [K, 2F]
+ *              (MXQ_ACT_SWIGLU: the gate's columns, then the other's) weights,
+ *              quantized with dim -2 to fmt (enum mxq_out_dtype; e2m1 has two bytes
+ *              a container, FP8 four).
+ *   w2, w2_scale   the same of [F, N].
+ *   K, F       multiples of 32; N a multiple of 4. An expert's matrix is below 2^31
+ *              values.
+ *   act        enum mxq_act.
+ *   workspace  mxq_moe_few_tokens_workspace_bytes() bytes; nothing in it has to hold
+ *              a value before the call. Calls that may run at the same time need
+ *              one each.
+ *   out        [tokens, N] of in_dtype.
+ * All pointers are device pointers, 16-byte aligned. Equal inputs give equal outputs.
+ */
+int mxq_moe_few_tokens(const void *x, int64_t tokens, int64_t K, int in_dtype, const void *ids, int id_bytes,
+                       const float *weights, int64_t slots, int64_t experts, const void *w1, const void *w1_scale,
+                       const void *w2, const void *w2_scale, int64_t F, int64_t N, int fmt, int act, void *workspace,
+                       void *out, void *stream);
 
 /* Workspace of mxq_clip_grad_norm; 0 for invalid arguments. The three arrays
  * are host memory. */

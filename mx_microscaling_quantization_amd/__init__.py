@@ -19,11 +19,10 @@ from typing import NamedTuple
 import torch  # loaded first so that the library binds to torch's HIP runtime
 
 __all__ = [
-    "IN_DTYPES", "OUT_DTYPES", "RES_DTYPES", "ELEM_DTYPES", "MXQError", "quantize", "dequantize", "quantize_axis",
+    "IN_DTYPES", "OUT_DTYPES", "RES_DTYPES", "ELEM_DTYPES", "ACTIVATIONS", "MXQError", "quantize", "dequantize", "quantize_axis",
     "scaled_matmul", "scaled_matmul_quantize", "MoEPlan", "moe_rows", "moe_sort", "moe_gather_quantize", "moe_combine",
-    "moe_combine_backward", "grouped_scaled_matmul", "grouped_scaled_matmul_wgrad", "scaled_matmul_fp4", "grouped_scaled_matmul_fp4",
-    "clip_grad_norm", "grad_norm",
-    "data_bytes", "scale_image_bytes", "result_bytes", "data_shape", "scale_image_shape",
+    "moe_combine_backward", "grouped_scaled_matmul", "grouped_scaled_matmul_wgrad", "scaled_matmul_fp4",
+    "grouped_scaled_matmul_fp4", "moe_few_tokens", "clip_grad_norm", "grad_norm", "data_bytes", "scale_image_bytes", "result_bytes", "data_shape", "scale_image_shape",
     "axis_view_shape", "logical_scale_view", "status_string", "library_path", "load",
 ]
 
@@ -34,6 +33,7 @@ IN_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 OUT_DTYPES = {"e4m3fn": 0, "e5m2": 1, "e2m1": 2}
 RES_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 ELEM_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTIVATIONS = {"silu": 0, "swiglu": 1}
 FLAG_ALT_EMAX = 1
 FLAG_DENSE_SCALE = 2
 ABI_VERSION = 1
@@ -118,6 +118,11 @@ def load():
         lib.mxq_scaled_matmul_fp4.restype = c.c_int
         lib.mxq_grouped_matmul_fp4.argtypes = [p, p, p, p, p, i64, i64, i64, i64, c.c_int, c.c_int, p, p]
         lib.mxq_grouped_matmul_fp4.restype = c.c_int
+        lib.mxq_moe_few_tokens_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        lib.mxq_moe_few_tokens_workspace_bytes.restype = c.c_size_t
+        lib.mxq_moe_few_tokens.argtypes = [p, i64, i64, c.c_int, p, c.c_int, p, i64, i64, p, p, p, p, i64, i64, c.c_int,
+                                           c.c_int, p, p, p]
+        lib.mxq_moe_few_tokens.restype = c.c_int
         lib.mxq_clip_grad_norm_workspace_bytes.argtypes = [p, p, i64]
         lib.mxq_clip_grad_norm_workspace_bytes.restype = c.c_size_t
         lib.mxq_clip_grad_norm.argtypes = [p, p, p, p, i64, c.c_double, p, p, p]
@@ -815,6 +820,77 @@ def grouped_scaled_matmul_fp4(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs: t
         _check_tensor("out", out, (M, N), (res_dtype,), dev)
     _check(_call_on(dev, lib.mxq_grouped_matmul_fp4, lhs.data_ptr(), lhs_scale.data_ptr(), rhs.data_ptr(),
                     rhs_scale.data_ptr(), offsets.data_ptr(), G, P, M, N, code, RES_DTYPES[res_dtype], out.data_ptr(),
+                    _stream_handle(stream, dev)))
+    if given:
+        _written(out)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# A whole layer for a few tokens
+# ---------------------------------------------------------------------------
+
+def _act_code(activation: str) -> int:
+    try:
+        return ACTIVATIONS[activation]
+    except KeyError:
+        raise MXQError(16, "activation must be one of %s" % sorted(ACTIVATIONS)) from None
+
+
+@functools.lru_cache(maxsize=256)
+def _few_nbytes(tokens: int, slots: int, F: int, N: int) -> int:
+    return int(load().mxq_moe_few_tokens_workspace_bytes(tokens, slots, F, N))
+
+
+def moe_few_tokens(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, w1: torch.Tensor,
+                   w1_scale: torch.Tensor, w2: torch.Tensor, w2_scale: torch.Tensor, fmt: str = "e2m1",
+                   activation: str = "swiglu", out: torch.Tensor | None = None,
+                   stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for the tokens of a decode step: out[t] = sum
+    over j of weights[t, j] * (act(x[t] @ W1_e) @ W2_e) with e = experts[t, j], in two
+    kernels.
+
+    ``x`` [tokens, K] is bf16 or f16, ``experts`` [tokens, slots] int32 or int64 (a number
+    outside 0 .. E - 1 adds nothing), ``weights`` [tokens, slots] float32; tokens * slots
+    is at most 1024. ``w1`` [E, K/4, ..] with dense scales [E, K/32, ..] are each
+    expert's [K, F] (``"silu"``) or [K, 2F] (``"swiglu"``: the gate's F columns, then the
+    other's) weights and ``w2``, ``w2_scale`` those of [F, N], quantized with
+    ``dim=-2, dense_scale=True`` to ``fmt``. The activations are not quantized. Returns
+    [tokens, N] of x's type.
+    """
+    lib = load()
+    code, act = _out_code(fmt), _act_code(activation)
+    if x.dtype not in IN_DTYPES:
+        raise MXQError(1, "input must be bfloat16 or float16, got %s" % x.dtype)
+    _check_tensor("x", x, 2, _IN)
+    dev = x.device
+    T, K = x.shape
+    _check_tensor("experts", experts, 2, _IDS, dev)
+    k = experts.shape[1]
+    if experts.shape[0] != T:
+        raise ValueError("x has %d rows, experts %d" % (T, experts.shape[0]))
+    _check_tensor("weights", weights, (T, k), _FLOAT32, dev)
+    _check_tensor("w1_scale", w1_scale, 3, _UINT8, dev)
+    _check_tensor("w2_scale", w2_scale, 3, _UINT8, dev)
+    E, blocks, width = w1_scale.shape
+    N = w2_scale.shape[2]
+    F = width // 2 if act else width
+    cb = _CONTAINER[fmt]
+    if blocks * 32 != K or (act and width % 2) or F % 32:
+        raise ValueError("w1_scale %s does not hold the scales of [%d, %s] weights" %
+                         (tuple(w1_scale.shape), K, "2 F" if act else "F"))
+    _check_tensor("w1", w1, (E, K // 4, cb * width), _UINT8, dev)
+    _check_tensor("w2_scale", w2_scale, (E, F // 32, N), _UINT8, dev)
+    _check_tensor("w2", w2, (E, F // 4, cb * N), _UINT8, dev)
+    given = out is not None
+    if not given:
+        out = _new((T, N), x.dtype, dev, stream)
+    else:
+        _check_tensor("out", out, (T, N), (x.dtype,), dev)
+    ws = _new((_few_nbytes(T, k, F, N),), torch.uint8, dev, stream)
+    _check(_call_on(dev, lib.mxq_moe_few_tokens, x.data_ptr(), T, K, IN_DTYPES[x.dtype], experts.data_ptr(),
+                    experts.element_size(), weights.data_ptr(), k, E, w1.data_ptr(), w1_scale.data_ptr(),
+                    w2.data_ptr(), w2_scale.data_ptr(), F, N, code, act, ws.data_ptr(), out.data_ptr(),
                     _stream_handle(stream, dev)))
     if given:
         _written(out)

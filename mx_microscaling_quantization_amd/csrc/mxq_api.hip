@@ -32,6 +32,7 @@ const char *mxq_status_string(int status)
     case MXQ_E_ROWS: return "sorted rows must be a non-negative multiple of 4, and counts non-negative";
     case MXQ_E_ELEM_DTYPE: return "element type must be BF16, F16 or F32 (expert numbers: int32 or int64)";
     case MXQ_E_VALUE: return "max_norm must not be negative or NaN";
+    case MXQ_E_ACT: return "activation must be silu or swiglu";
     default: return "unknown status";
     }
 }
