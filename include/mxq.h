@@ -534,6 +534,53 @@ int mxq_moe_few_tokens(const void *x, int64_t tokens, int64_t K, int in_dtype, c
                        const void *w2, const void *w2_scale, int64_t F, int64_t N, int fmt, int act, void *workspace,
                        void *out, void *stream);
 
+/*
+ * mxq_act_quantize -- the activation between two products on MX operands:
+ *     h = silu(z) of z [R, F], or silu(z[:, :F]) * z[:, F:] of z [R, 2F]
+ * computed in fp32 and rounded to z's type, in one pass that writes
+ *   - h quantized along its rows: the bytes mxq_quantize_axis(h, dim -1) gives with
+ *     dense scales, the left operand of the next product;
+ *   - z in 8 bits for the backward pass: the bytes mxq_quantize_ex(z) gives with dense
+ *     scales (8 x 4 blocks), which mxq_dequantize_ex decodes.
+ *
+ *   z            device pointer, [R, W] of in_dtype (enum mxq_in_dtype); W = F
+ *                (MXQ_ACT_SILU) or 2F (MXQ_ACT_SWIGLU: the gate's columns first).
+ *   R            multiple of 8; F a multiple of 32 (MXQ_E_SHAPE_P8). Empty: a no-op.
+ *   out_dtype    enum mxq_out_dtype of h.
+ *   saved_dtype  MXQ_OUT_E4M3FN or MXQ_OUT_E5M2.
+ *   act          enum mxq_act.
+ *   data_out, scale_out   mxq_data_bytes(F/4, 4R, out_dtype) and F/32 * R bytes.
+ *   saved, saved_scale    R * W and R/8 * W/4 bytes.
+ * All pointers 16-byte aligned.
+ */
+int mxq_act_quantize(const void *z, int64_t R, int64_t F, int in_dtype, int out_dtype, int saved_dtype, int act,
+                     void *data_out, void *scale_out, void *saved, void *saved_scale, void *stream);
+
+/*
+ * mxq_act_quantize_backward -- the activation's backward pass from the kept z, in one
+ * pass. With z~ the decoded z (every scale byte at its value, 255 included), g and u
+ * its columns, s = 1 / (1 + e^-g) and grad the gradient of h:
+ *     dz = grad * s (1 + g (1 - s))                                  (MXQ_ACT_SILU)
+ *     dz = [grad * u * s (1 + g (1 - s)), grad * g s]                (MXQ_ACT_SWIGLU)
+ *     h  = act(z~)
+ * computed in fp32 and rounded to grad's type, then quantized:
+ *   rows_data, rows_scale   dz along its rows (dim -1): for the product that gives
+ *                           the first product's input gradient.
+ *   cols_data, cols_scale   dz down its columns (dim -2): for the gradient of the first
+ *                           weights (mxq_grouped_matmul_wgrad's rhs).
+ *   h_data, h_scale         h down its columns: for the gradient of the second
+ *                           weights (its lhs), so that h need not be kept either.
+ * each as mxq_quantize_axis writes it with dense scales.
+ *
+ *   grad         device pointer, [R, F] of in_dtype.
+ *   R, F         multiples of 32.
+ *   the rest     as for mxq_act_quantize; data of W R values (rows, cols) and F R (h).
+ * All pointers 16-byte aligned.
+ */
+int mxq_act_quantize_backward(const void *grad, const void *saved, const void *saved_scale, int64_t R, int64_t F,
+                              int in_dtype, int out_dtype, int saved_dtype, int act, void *rows_data, void *rows_scale,
+                              void *cols_data, void *cols_scale, void *h_data, void *h_scale, void *stream);
+
 /* Workspace of mxq_clip_grad_norm; 0 for invalid arguments. The three arrays
  * are host memory. */
 size_t mxq_clip_grad_norm_workspace_bytes(const int64_t *elements, const int *elem_dtypes, int64_t count);

@@ -22,7 +22,8 @@ __all__ = [
     "IN_DTYPES", "OUT_DTYPES", "RES_DTYPES", "ELEM_DTYPES", "ACTIVATIONS", "MXQError", "quantize", "dequantize", "quantize_axis",
     "scaled_matmul", "scaled_matmul_quantize", "MoEPlan", "moe_rows", "moe_sort", "moe_gather_quantize", "moe_combine",
     "moe_combine_backward", "grouped_scaled_matmul", "grouped_scaled_matmul_wgrad", "scaled_matmul_fp4",
-    "grouped_scaled_matmul_fp4", "moe_few_tokens", "clip_grad_norm", "grad_norm", "data_bytes", "scale_image_bytes", "result_bytes", "data_shape", "scale_image_shape",
+    "grouped_scaled_matmul_fp4", "moe_few_tokens", "ActGradients", "act_quantize", "act_quantize_backward",
+    "clip_grad_norm", "grad_norm", "data_bytes", "scale_image_bytes", "result_bytes", "data_shape", "scale_image_shape",
     "axis_view_shape", "logical_scale_view", "status_string", "library_path", "load",
 ]
 
@@ -123,6 +124,11 @@ def load():
         lib.mxq_moe_few_tokens.argtypes = [p, i64, i64, c.c_int, p, c.c_int, p, i64, i64, p, p, p, p, i64, i64, c.c_int,
                                            c.c_int, p, p, p]
         lib.mxq_moe_few_tokens.restype = c.c_int
+        lib.mxq_act_quantize.argtypes = [p, i64, i64, c.c_int, c.c_int, c.c_int, c.c_int, p, p, p, p, p]
+        lib.mxq_act_quantize.restype = c.c_int
+        lib.mxq_act_quantize_backward.argtypes = [p, p, p, i64, i64, c.c_int, c.c_int, c.c_int, c.c_int, p, p, p, p, p, p,
+                                                  p]
+        lib.mxq_act_quantize_backward.restype = c.c_int
         lib.mxq_clip_grad_norm_workspace_bytes.argtypes = [p, p, i64]
         lib.mxq_clip_grad_norm_workspace_bytes.restype = c.c_size_t
         lib.mxq_clip_grad_norm.argtypes = [p, p, p, p, i64, c.c_double, p, p, p]
@@ -895,6 +901,91 @@ def moe_few_tokens(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor
     if given:
         _written(out)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Activations between products, kept in 8 bits
+# ---------------------------------------------------------------------------
+
+def _saved_code(saved_dtype: str) -> int:
+    if saved_dtype not in ("e4m3fn", "e5m2"):
+        raise MXQError(2, "activations are kept in e4m3fn or e5m2, not %r" % (saved_dtype,))
+    return OUT_DTYPES[saved_dtype]
+
+
+def act_quantize(z: torch.Tensor, activation: str = "swiglu", out_dtype: str = "e4m3fn", saved_dtype: str = "e4m3fn",
+                 stream: torch.cuda.Stream | None = None):
+    """The activation h of a product's result ``z`` (bf16 or f16), quantized for the next
+    product, and z in 8 bits for :func:`act_quantize_backward`, in one pass.
+
+    ``"silu"``: h = silu(z) of z [R, F]; ``"swiglu"``: h = silu(z[:, :F]) * z[:, F:] of
+    z [R, 2F]; float32, rounded to z's type. R is a multiple of 8, F of 32. Returns
+    ``((data, scale), (saved, saved_scale))``: what :func:`quantize_axis` with ``dim=-1``
+    gives for h, and what :func:`quantize` gives for z (:func:`dequantize` decodes it),
+    both with dense scales.
+    """
+    lib = load()
+    act, code, saved_code = _act_code(activation), _out_code(out_dtype), _saved_code(saved_dtype)
+    if z.dtype not in IN_DTYPES:
+        raise MXQError(1, "input must be bfloat16 or float16, got %s" % z.dtype)
+    _check_tensor("z", z, 2, _IN)
+    R, W = z.shape
+    F = W // 2 if act else W
+    if R % 8 or F % 32 or (act and W % 2):
+        raise MXQError(3, "z must be [R, %s] with R a multiple of 8 and F of 32, got shape %s" %
+                       ("2 F" if act else "F", tuple(z.shape)))
+    dev = z.device
+    data = _new((F // 4, _CONTAINER[out_dtype] * R), torch.uint8, dev, stream)
+    scale = _new((F // 32, R), torch.uint8, dev, stream)
+    saved = _new((R, W), torch.uint8, dev, stream)
+    saved_scale = _new((R // 8, W // 4), torch.uint8, dev, stream)
+    _check(_call_on(dev, lib.mxq_act_quantize, z.data_ptr(), R, F, IN_DTYPES[z.dtype], code, saved_code, act,
+                    data.data_ptr(), scale.data_ptr(), saved.data_ptr(), saved_scale.data_ptr(),
+                    _stream_handle(stream, dev)))
+    return (data, scale), (saved, saved_scale)
+
+
+class ActGradients(NamedTuple):
+    """What :func:`act_quantize_backward` gives, each ``(data, scale)`` as
+    :func:`quantize_axis` writes it with dense scales."""
+
+    rows: tuple    # dz along its rows (dim -1)
+    cols: tuple    # dz down its columns (dim -2)
+    h: tuple       # the activation down its columns (dim -2)
+
+
+def act_quantize_backward(grad: torch.Tensor, saved: torch.Tensor, saved_scale: torch.Tensor,
+                          activation: str = "swiglu", saved_dtype: str = "e4m3fn", out_dtype: str = "e4m3fn",
+                          stream: torch.cuda.Stream | None = None) -> ActGradients:
+    """The backward pass of :func:`act_quantize` from the z it kept, in one pass: with
+    ``grad`` [R, F] (bf16 or f16) the gradient of h, the gradient dz of z quantized along
+    its rows (for the input's gradient, :func:`grouped_scaled_matmul`) and down its columns
+    (for the first weights', :func:`grouped_scaled_matmul_wgrad`), and h down its columns
+    (for the second weights').
+
+    dz and h are those of the decoded z, float32 rounded to grad's type before they are
+    quantized. R and F are multiples of 32.
+    """
+    lib = load()
+    act, code, saved_code = _act_code(activation), _out_code(out_dtype), _saved_code(saved_dtype)
+    if grad.dtype not in IN_DTYPES:
+        raise MXQError(1, "grad must be bfloat16 or float16, got %s" % grad.dtype)
+    _check_tensor("grad", grad, 2, _IN)
+    R, F = grad.shape
+    if R % 32 or F % 32:
+        raise MXQError(3, "grad must be [R, F] with multiples of 32, got shape %s" % (tuple(grad.shape),))
+    W = 2 * F if act else F
+    dev = grad.device
+    _check_tensor("saved", saved, (R, W), _UINT8, dev)
+    _check_tensor("saved_scale", saved_scale, (R // 8, W // 4), _UINT8, dev)
+    cb = _CONTAINER[out_dtype]
+    rows = (_new((W // 4, cb * R), torch.uint8, dev, stream), _new((W // 32, R), torch.uint8, dev, stream))
+    cols = (_new((R // 4, cb * W), torch.uint8, dev, stream), _new((R // 32, W), torch.uint8, dev, stream))
+    h = (_new((R // 4, cb * F), torch.uint8, dev, stream), _new((R // 32, F), torch.uint8, dev, stream))
+    _check(_call_on(dev, lib.mxq_act_quantize_backward, grad.data_ptr(), saved.data_ptr(), saved_scale.data_ptr(), R, F,
+                    IN_DTYPES[grad.dtype], code, saved_code, act, *(t.data_ptr() for t in rows + cols + h),
+                    _stream_handle(stream, dev)))
+    return ActGradients(rows, cols, h)
 
 
 # ---------------------------------------------------------------------------

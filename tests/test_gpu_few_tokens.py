@@ -4,8 +4,9 @@ bits on the same quantized weights.
 Bounds, for unit u = 2^-24 and a result y = sum_j w_j sum_f h_f W2_f with h = act(z):
 a product's fp32 sum of K terms is off by at most (K + 10) u of the sum of its terms'
 magnitudes (each addition by half a step of a partial sum; 8 waves' sums are added on top).
-silu is off by |z| u from the exponential's argument and a few u from the rest, taken
-as (|z| + 8) u of its magnitude; its slope is at most 1.1 in magnitude, so an error d in z
+The exponential's argument z log2(e) is off by two roundings, 2 |z| u in the
+exponential's relative error, and the steps from there to silu by 7 u more (exponential
+and reciprocal a whole step each, sum, product): (2 |z| + 8) u of its magnitude; its slope is at most 1.1 in magnitude, so an error d in z
 gives at most 1.1 d. h is kept to 2^-17 of its value (two bf16 numbers: half a step of 2^-8
 of what the first one leaves, at most 2^-9 of the value). The result is rounded once,
 by at most half a step of its type.
@@ -53,7 +54,7 @@ def reference(x, ids, weights, w1, w2, act):
             F = w2[e].shape[0]
             gate, dg = z[:F], dz[:F]
             s = gate / (1.0 + np.exp(-gate))
-            ds = 1.1 * dg + (np.abs(gate) + 8) * U * np.abs(s)
+            ds = 1.1 * dg + (2 * np.abs(gate) + 8) * U * np.abs(s)
             if act == "swiglu":
                 h = s * z[F:]
                 dh = ds * np.abs(z[F:]) + np.abs(s) * dz[F:] + ds * dz[F:] + U * np.abs(h)
