@@ -12,37 +12,44 @@ namespace {
 using mxq_host::grid_fits;
 
 typedef void (*up_fn)(const uint16_t *, uint32_t, const void *, uint32_t, uint32_t, uint32_t, const uint8_t *,
-                      const uint8_t *, uint32_t, uint32_t, uint16_t *, uint32_t *, uint32_t);
+                      const uint8_t *, uint32_t, uint32_t, uint16_t *, uint32_t *, uint32_t, uint16_t *, uint32_t);
 typedef void (*down_fn)(const uint16_t *, uint32_t, const void *, uint32_t, uint32_t, uint32_t, const uint8_t *,
                         const uint8_t *, uint32_t, uint32_t, float *, uint32_t *, const float *, uint16_t *);
 
-template <int FMT, int IN, typename ID> up_fn pick_act(int act)
+struct Kernels {
+    up_fn up;
+    down_fn down;
+};
+
+template <int FMT, int IN, int MX, typename ID> Kernels pick_act(int act)
 {
-    return act == MXQ_ACT_SWIGLU ? (up_fn)mxq::few_up_kernel<FMT, IN, mxq::kActSwiglu, ID>
-                                 : (up_fn)mxq::few_up_kernel<FMT, IN, mxq::kActSilu, ID>;
+    return {act == MXQ_ACT_SWIGLU ? (up_fn)mxq::few_up_kernel<FMT, IN, mxq::kActSwiglu, MX, ID>
+                                  : (up_fn)mxq::few_up_kernel<FMT, IN, mxq::kActSilu, MX, ID>,
+            mxq::few_down_kernel<FMT, IN, MX, ID>};
 }
 
-template <int FMT, int IN> void pick_id(int id_bytes, int act, up_fn &up, down_fn &down)
+template <int FMT, int IN, int MX> Kernels pick_id(int id_bytes, int act)
 {
-    up = id_bytes == 8 ? pick_act<FMT, IN, int64_t>(act) : pick_act<FMT, IN, int32_t>(act);
-    down = id_bytes == 8 ? (down_fn)mxq::few_down_kernel<FMT, IN, int64_t>
-                         : (down_fn)mxq::few_down_kernel<FMT, IN, int32_t>;
+    return id_bytes == 8 ? pick_act<FMT, IN, MX, int64_t>(act) : pick_act<FMT, IN, MX, int32_t>(act);
 }
 
-template <int FMT> void pick_in(int in_dtype, int id_bytes, int act, up_fn &up, down_fn &down)
+template <int FMT, int IN> Kernels pick_rows(bool many, int id_bytes, int act)
 {
-    if (in_dtype == MXQ_IN_BF16)
-        pick_id<FMT, mxq::kInBF16>(id_bytes, act, up, down);
-    else
-        pick_id<FMT, mxq::kInF16>(id_bytes, act, up, down);
+    return many ? pick_id<FMT, IN, 4>(id_bytes, act) : pick_id<FMT, IN, 2>(id_bytes, act);
 }
 
-void pick(int fmt, int in_dtype, int id_bytes, int act, up_fn &up, down_fn &down)
+template <int FMT> Kernels pick_in(int in_dtype, bool many, int id_bytes, int act)
+{
+    return in_dtype == MXQ_IN_BF16 ? pick_rows<FMT, mxq::kInBF16>(many, id_bytes, act)
+                                   : pick_rows<FMT, mxq::kInF16>(many, id_bytes, act);
+}
+
+Kernels pick(int fmt, int in_dtype, bool many, int id_bytes, int act)
 {
     switch (fmt) {
-    case MXQ_OUT_E4M3FN: return pick_in<mxq::kOutE4M3FN>(in_dtype, id_bytes, act, up, down);
-    case MXQ_OUT_E5M2: return pick_in<mxq::kOutE5M2>(in_dtype, id_bytes, act, up, down);
-    default: return pick_in<mxq::kOutE2M1>(in_dtype, id_bytes, act, up, down);
+    case MXQ_OUT_E4M3FN: return pick_in<mxq::kOutE4M3FN>(in_dtype, many, id_bytes, act);
+    case MXQ_OUT_E5M2: return pick_in<mxq::kOutE5M2>(in_dtype, many, id_bytes, act);
+    default: return pick_in<mxq::kOutE2M1>(in_dtype, many, id_bytes, act);
     }
 }
 
@@ -65,7 +72,15 @@ int check_sizes(int64_t tokens, int64_t K, int64_t slots, int64_t experts, int64
 
 int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-int64_t tiles_of(int64_t cols) { return (cols + mxq::kFewCols - 1) / mxq::kFewCols; }
+int64_t tiles_of(int64_t cols, int fmt)
+{
+    const int64_t tile = fmt == MXQ_OUT_E2M1 ? mxq::FewCols<mxq::kOutE2M1>::all : mxq::FewCols<mxq::kOutE4M3FN>::all;
+    return (cols + tile - 1) / tile;
+}
+
+// Waves of a workgroup: eight share a contraction where there are few workgroups, four
+// where there are enough of them to fill the CUs' places.
+uint32_t waves_of(int64_t workgroups) { return workgroups > 256 ? 4u : 8u; }
 
 } // namespace
 
@@ -76,7 +91,7 @@ size_t mxq_moe_few_tokens_workspace_bytes(int64_t tokens, int64_t slots, int64_t
     if (check_sizes(tokens, 0, slots, 1, F, N) != MXQ_OK)
         return 0;
     const int64_t pairs = tokens * slots;
-    return (size_t)(round16(4 * pairs * F) + round16(4 * pairs * N) + round16(4 * tiles_of(N)));
+    return (size_t)(round16(4 * pairs * F) + round16(4 * pairs * N) + round16(4 * tiles_of(N, MXQ_OUT_E4M3FN) * tokens));
 }
 
 int mxq_moe_few_tokens(const void *x, int64_t tokens, int64_t K, int in_dtype, const void *ids, int id_bytes,
@@ -105,25 +120,25 @@ int mxq_moe_few_tokens(const void *x, int64_t tokens, int64_t K, int in_dtype, c
     uint32_t pairs = (uint32_t)(tokens * slots), s = (uint32_t)slots, e = (uint32_t)experts;
     uint32_t k = (uint32_t)K, f = (uint32_t)F, n = (uint32_t)N;
     // as many workgroups as any assignment has experts in use; at least one column tile
-    // of the first kernel, which clears the second one's counters
+    // of the first kernel, which also prepares the second one's counters
     const int64_t used = pairs < e ? pairs : e;
-    const int64_t up_tiles = F > 0 ? tiles_of(F) : 1, down_tiles = tiles_of(N);
+    const int64_t up_tiles = F > 0 ? tiles_of(F, fmt) : 1, down_tiles = tiles_of(N, fmt);
     if (!grid_fits(used, up_tiles, mxq::kFewThreads) || !grid_fits(used, down_tiles, mxq::kFewThreads))
         return MXQ_E_OVERFLOW;
+    const uint32_t up_waves = waves_of(used * up_tiles), down_waves = waves_of(used * down_tiles);
+    const uint32_t lds = 4u * 16u * 64u;      // a wave's sums of a part with one matrix
     uint32_t ut = (uint32_t)up_tiles, dt = (uint32_t)down_tiles;
     uint16_t *h = (uint16_t *)workspace;
     float *y = (float *)((uint8_t *)workspace + round16(4 * (int64_t)pairs * F));
     uint32_t *arrived = (uint32_t *)((uint8_t *)y + round16(4 * (int64_t)pairs * N));
-    up_fn up;
-    down_fn down;
-    pick(fmt, in_dtype, id_bytes, act, up, down);
-    void *a1[] = {&x, &k, &ids, &pairs, &s, &e, &w1, &w1_scale, &f, &ut, &h, &arrived, &dt};
-    if (hipLaunchKernel((const void *)up, dim3((uint32_t)(used * up_tiles)), dim3(mxq::kFewThreads), a1, 0,
-                        (hipStream_t)stream) != hipSuccess)
+    const Kernels kernels = pick(fmt, in_dtype, pairs > 24 * used, id_bytes, act);
+    void *a1[] = {&x, &k, &ids, &pairs, &s, &e, &w1, &w1_scale, &f, &ut, &h, &arrived, &dt, &out, &n};
+    if (hipLaunchKernel((const void *)kernels.up, dim3((uint32_t)(used * up_tiles)), dim3(64u * up_waves), a1,
+                        up_waves * lds * (act == MXQ_ACT_SWIGLU ? 2u : 1u), (hipStream_t)stream) != hipSuccess)
         return MXQ_E_HIP;
     void *a2[] = {&h, &f, &ids, &pairs, &s, &e, &w2, &w2_scale, &n, &dt, &y, &arrived, &weights, &out};
-    const hipError_t err = hipLaunchKernel((const void *)down, dim3((uint32_t)(used * down_tiles)),
-                                           dim3(mxq::kFewThreads), a2, 0, (hipStream_t)stream);
+    const hipError_t err = hipLaunchKernel((const void *)kernels.down, dim3((uint32_t)(used * down_tiles)),
+                                           dim3(64u * down_waves), a2, down_waves * lds, (hipStream_t)stream);
     return err == hipSuccess ? MXQ_OK : MXQ_E_HIP;
 }
 

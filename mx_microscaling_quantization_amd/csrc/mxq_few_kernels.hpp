@@ -38,97 +38,105 @@ typedef float f32x2_t __attribute__((ext_vector_type(2)));
 enum { kActSilu = 0, kActSwiglu = 1 };
 
 constexpr uint32_t kFewPairs = 1024;     // pairs a workgroup finds its expert among
-constexpr uint32_t kFewWaves = 8;        // waves that share the contraction
+constexpr uint32_t kFewWaves = 8;        // waves that share the contraction, at most
 constexpr uint32_t kFewThreads = 64 * kFewWaves;
-constexpr uint32_t kFewCols = 64;        // columns of a workgroup: 16 lanes x 4
-constexpr int kFewU = 4;
+
+// Columns of a lane.
+template <int FMT> struct FewCols {
+    static constexpr int lane = 4;
+    static constexpr uint32_t all = 16u * lane;     // of a workgroup
+};
 
 // ----------------------------------------------------------------------------
 // Which expert, which pairs
 // ----------------------------------------------------------------------------
 
 struct FewRoute {
-    uint32_t mask[32];                   // experts in use
-    uint32_t counts[kFewPairs / 64];     // pairs of this workgroup's expert per 64 ids
+    uint8_t used[kFewWaves][1024];       // experts in use, a byte each; every wave has its own copy
+    uint32_t count;                      // pairs of this workgroup's expert, in order
     uint16_t pairs[kFewPairs];
 };
 
-// The `a`-th expert in use (in order of its number): its number and its count of
-// pairs, which are then in route.pairs in order; `active` experts are in use. False where
-// there is no a-th one. Every thread of the workgroup takes part.
+// This workgroup's place: one of the experts in use (in order of their numbers; `active`
+// of them are), its pairs, which are then in route.pairs in order, and a column tile. Each
+// XCD gets consecutive places, so that a line of weights that two column tiles share is
+// read into one L2. False where there is no place for this workgroup. Every thread of the
+// workgroup takes part. Each wave finds the expert by itself, so that one barrier is all
+// (the list of pairs, by wave 0).
+struct FewPlace {
+    uint32_t expert, count, tile, active;
+};
+
 template <typename ID>
-__device__ __forceinline__ bool few_route(FewRoute &route, const void *ids_, uint32_t n, uint32_t experts, uint32_t a,
-                                          uint32_t &expert, uint32_t &count, uint32_t &active)
+__device__ __forceinline__ bool few_route(FewRoute &route, const void *ids_, uint32_t n, uint32_t experts,
+                                          uint32_t tiles, FewPlace &place)
 {
     const ID *ids = reinterpret_cast<const ID *>(ids_);
-    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-    constexpr uint32_t per = kFewPairs / kFewThreads;
-    if (tid < 32u)
-        route.mask[tid] = 0;
-    __syncthreads();
-    uint32_t mine[per];
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr uint32_t per = kFewPairs / 64u;
+    volatile uint8_t *used = route.used[wave];
+    ID id[per];
 #pragma unroll
-    for (uint32_t q = 0; q < per; q++) {
-        const uint32_t p = q * kFewThreads + tid;
-        mine[q] = 0xFFFFFFFFu;
-        if (p < n) {
-            const ID id = ids[p];
-            if (id >= 0 && (uint64_t)id < experts) {
-                mine[q] = (uint32_t)id;
-                atomicOr(&route.mask[mine[q] >> 5], 1u << (mine[q] & 31u));
-            }
-        }
-    }
-    __syncthreads();
-    // lane l < 32 scans the bits of word l
-    const uint32_t word = lane < 32u ? route.mask[lane] : 0u;
-    uint32_t before = __popc(word);
+    for (uint32_t q = 0; q < per; q++)
+        if (64u * q < n)
+            id[q] = ids[min(64u * q + lane, n - 1u)];
+    // (bytes, not bits: lanes that name one expert write the same byte, where atomic ors of
+    // one word go one after the other, 5 us for 366 pairs of 64 experts)
+    volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(used);
+#pragma unroll
+    for (uint32_t k = 0; k < 4; k++)
+        words[64u * k + lane] = 0;
+#pragma unroll
+    for (uint32_t q = 0; q < per; q++)
+        if (64u * q < n && id[q] >= 0 && (uint64_t)id[q] < experts)
+            used[id[q]] = 1;
+    // lane l has experts 16 l .. 16 l + 15
+    uint32_t flags = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; k++)     // four bytes of 0 or 1 to four bits
+        flags |= ((words[4u * lane + k] * 0x01020408u) >> 24) << (4u * k);
+    uint32_t before = __popc(flags);
     const uint32_t own = before;
 #pragma unroll
-    for (uint32_t d = 1; d < 32; d <<= 1) {
+    for (uint32_t d = 1; d < 64; d <<= 1) {
         const uint32_t o = (uint32_t)__shfl_up((int)before, d);
         before += lane >= d ? o : 0u;
     }
-    active = (uint32_t)__builtin_amdgcn_readlane((int)before, 31);
+    place.active = (uint32_t)__builtin_amdgcn_readlane((int)before, 63);
     before -= own;
-    if (a >= active)
+    const uint32_t t = xcd_tile(blockIdx.x, place.active * tiles);
+    const uint32_t a = t / tiles;
+    place.tile = t - a * tiles;
+    if (a >= place.active)
         return false;
-    // the lane whose word holds the a-th bit
+    // the lane that has the a-th of them
     uint32_t bit = 0;
-    const bool here = lane < 32u && a >= before && a < before + own;
+    const bool here = a >= before && a < before + own;
     if (here) {
-        uint32_t w = word;
         for (uint32_t k = a - before; k > 0; k--)
-            w &= w - 1u;
-        bit = 32u * lane + (uint32_t)__builtin_ctz(w);
+            flags &= flags - 1u;
+        bit = 16u * lane + (uint32_t)__builtin_ctz(flags);
     }
     const uint32_t at = (uint32_t)__builtin_ctzll(__builtin_amdgcn_ballot_w64(here));
-    expert = (uint32_t)__builtin_amdgcn_readlane((int)bit, (int)at);
-    uint64_t match[per];
-#pragma unroll
-    for (uint32_t q = 0; q < per; q++) {
-        match[q] = __builtin_amdgcn_ballot_w64(mine[q] == expert);
-        if (lane == 0)
-            route.counts[q * kFewWaves + wave] = (uint32_t)__popcll(match[q]);
-    }
-    __syncthreads();
-    count = 0;
-    uint32_t first[per];
-#pragma unroll
-    for (uint32_t c = 0; c < kFewPairs / 64u; c++) {
+    place.expert = (uint32_t)__builtin_amdgcn_readlane((int)bit, (int)at);
+    if (wave == 0) {
+        uint32_t count = 0;
 #pragma unroll
         for (uint32_t q = 0; q < per; q++)
-            if (c == q * kFewWaves + wave)
-                first[q] = count;
-        count += route.counts[c];
+            if (64u * q < n) {
+                const bool mine = 64u * q + lane < n && id[q] == (ID)place.expert;
+                const uint64_t match = __builtin_amdgcn_ballot_w64(mine);
+                if (mine)
+                    route.pairs[count + (uint32_t)__popcll(match & ((1ull << lane) - 1ull))] =
+                        (uint16_t)(64u * q + lane);
+                count += (uint32_t)__popcll(match);
+            }
+        if (lane == 0)
+            route.count = count;
     }
-#pragma unroll
-    for (uint32_t q = 0; q < per; q++)
-        if (mine[q] == expert)
-            route.pairs[first[q] + (uint32_t)__popcll(match[q] & ((1ull << lane) - 1ull))] =
-                (uint16_t)(q * kFewThreads + tid);
     __syncthreads();
-    count = (uint32_t)__builtin_amdgcn_readfirstlane((int)count);
+    place.count = (uint32_t)__builtin_amdgcn_readfirstlane((int)route.count);
     return true;
 }
 
@@ -143,12 +151,12 @@ struct FewMatrix {
 };
 
 template <int FMT> struct FewBlock {
-    static constexpr int dwords = FMT == kOutE2M1 ? 2 : 4;
-    uint32_t v[2][dwords];   // containers of view rows 2 g and 2 g + 1, four columns
-    uint32_t scale;          // E8M0 of the four columns
+    static constexpr int dwords = FewCols<FMT>::lane * (FMT == kOutE2M1 ? 2 : 4) / 4;
+    uint32_t v[2][dwords];                       // containers of view rows 2 g and 2 g + 1
+    uint32_t scale[FewCols<FMT>::lane / 4];      // E8M0 of the columns
 };
 
-// Block b, columns col .. col + 3 (an offset past every buffer where the lane has none).
+// Block b, the lane's columns from its offsets on (past every buffer where it has none).
 template <int FMT>
 __device__ __forceinline__ void few_load(FewBlock<FMT> &r, const __amdgpu_buffer_rsrc_t &data,
                                          const __amdgpu_buffer_rsrc_t &scale, uint32_t C, uint32_t b, uint32_t at_data,
@@ -158,7 +166,7 @@ __device__ __forceinline__ void few_load(FewBlock<FMT> &r, const __amdgpu_buffer
 #pragma unroll
     for (int q = 0; q < 2; q++) {
         const uint32_t row = (8u * b + q) * CB * C;
-        if constexpr (FMT == kOutE2M1) {
+        if constexpr (FewBlock<FMT>::dwords == 2) {
             const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(data, at_data, row, kBufferNT);
             r.v[q][0] = w.x;
             r.v[q][1] = w.y;
@@ -169,13 +177,20 @@ __device__ __forceinline__ void few_load(FewBlock<FMT> &r, const __amdgpu_buffer
                 r.v[q][k] = w[k];
         }
     }
-    r.scale = __builtin_amdgcn_raw_buffer_load_b32(scale, at_scale, b * C, 0);
+    if constexpr (FewCols<FMT>::lane == 8) {
+        const u32x2_t e = __builtin_amdgcn_raw_buffer_load_b64(scale, at_scale, b * C, 0);
+        r.scale[0] = e.x;
+        r.scale[1] = e.y;
+    } else {
+        r.scale[0] = __builtin_amdgcn_raw_buffer_load_b32(scale, at_scale, b * C, 0);
+    }
 }
 
 // Column u's 8 values times their scale, as bf16.
 template <int FMT> __device__ __forceinline__ bf16x8_t few_widen(const FewBlock<FMT> &r, int u)
 {
-    const float s = __uint_as_float((u < 3 ? r.scale << (23 - 8 * u) : r.scale >> 1) & 0x7F800000u);
+    const uint32_t e = r.scale[u >> 2];
+    const float s = __uint_as_float(((u & 3) < 3 ? e << (23 - 8 * (u & 3)) : e >> 1) & 0x7F800000u);
     bf16x2_t p[4];
     if constexpr (FMT == kOutE2M1) {
         // byte 1 of a container holds elements 0 and 1, byte 0 elements 2 and 3
@@ -228,13 +243,12 @@ __device__ __forceinline__ void few_left(FewLeft<IN> &r, const uint16_t *row, ui
         r.v[1] = *reinterpret_cast<const u32x4_t *>(row + plane + k);
 }
 
-// Two fp32 values as the bf16 pairs whose sums are nearest to them.
+// Two fp32 values as the bf16 pairs whose sums are nearest to them. (What an infinity
+// leaves is a NaN, and the results that it reaches are computed again, see few_exact.)
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t &high, uint32_t &low)
 {
     high = bf16_pair(a, b);
-    const float ha = __uint_as_float(high << 16), hb = __uint_as_float(high & 0xFFFF0000u);
-    // (an infinity has no second part)
-    low = bf16_pair(__builtin_isfinite(ha) ? a - ha : 0.0f, __builtin_isfinite(hb) ? b - hb : 0.0f);
+    low = bf16_pair(a - __uint_as_float(high << 16), b - __uint_as_float(high & 0xFFFF0000u));
 }
 
 template <int IN> __device__ __forceinline__ void few_terms(const FewLeft<IN> &r, bf16x8_t (&t)[FewRows<IN>::terms])
@@ -291,7 +305,7 @@ __device__ __attribute__((noinline)) float few_exact(const uint8_t *data, const 
             else
                 x = __uint_as_float((uint32_t)row[4u * p + k] << 16);
             if constexpr (IN == kInSplit)
-                x += __uint_as_float((uint32_t)row[plane + 4u * p + k] << 16);
+                x += __builtin_isfinite(x) ? __uint_as_float((uint32_t)row[plane + 4u * p + k] << 16) : 0.0f;
             sum += __builtin_ldexp((double)v[k >> 1][k & 1] * x, e);
         }
     }
@@ -299,40 +313,44 @@ __device__ __attribute__((noinline)) float few_exact(const uint8_t *data, const 
 }
 
 // ----------------------------------------------------------------------------
-// The products of one expert's pairs with 64 columns of NM matrices
+// The products of one expert's pairs with the columns of a workgroup of NM matrices
 // ----------------------------------------------------------------------------
 
-// MT tiles of 16 pairs from pair `first` on. Wave w takes the MX blocks w, w + 8, .. of the
-// contraction, `DEPTH` of them in flight, and leaves its sums in registers.
+// Blocks in flight, activations and weights alike: loads return in order, so waiting for
+// a later block's activations would be waiting for the weights before them.
+constexpr int few_depth(int MT) { return MT == 1 ? 4 : MT == 2 ? 3 : 2; }
+
+// MT tiles of 16 pairs from pair `first` on. Wave w takes the MX blocks w, w + waves, .. of the
+// contraction and leaves its sums in registers.
 template <int FMT, int IN, int NM, int MT>
-__device__ __forceinline__ void few_sums(f32x4_t (&acc)[MT][NM][kFewU], const __amdgpu_buffer_rsrc_t &data,
+__device__ __forceinline__ void few_sums(f32x4_t (&acc)[MT][NM][FewCols<FMT>::lane], const __amdgpu_buffer_rsrc_t &data,
                                          const __amdgpu_buffer_rsrc_t &scale, uint32_t C, uint32_t blocks,
                                          const uint32_t (&at_data)[NM], const uint32_t (&at_scale)[NM],
-                                         const uint16_t *const (&rows)[MT], uint64_t plane, uint32_t wave, uint32_t g)
+                                         const uint16_t *const (&rows)[MT], uint64_t plane, uint32_t wave, uint32_t waves, uint32_t g)
 {
-    constexpr int DEPTH = MT == 4 ? 2 : 4;
+    constexpr int D = few_depth(MT);
     constexpr int terms = FewRows<IN>::terms;
-    FewBlock<FMT> w[DEPTH][NM];
-    FewLeft<IN> x[DEPTH][MT];
-    const uint32_t n = blocks > wave ? (blocks - wave + kFewWaves - 1) / kFewWaves : 0u;
+    FewBlock<FMT> w[D][NM];
+    FewLeft<IN> x[D][MT];
+    const uint32_t n = blocks > wave ? (blocks - wave + waves - 1u) / waves : 0u;
     if (n == 0)
         return;
     const auto fetch = [&](int q, uint32_t s) {
-        const uint32_t b = wave + kFewWaves * min(s, n - 1u);   // (past the end: the last one again, not used)
-#pragma unroll
-        for (int k = 0; k < NM; k++)
-            few_load<FMT>(w[q][k], data, scale, C, b, at_data[k], at_scale[k]);
+        const uint32_t b = wave + waves * min(s, n - 1u);   // (past the end: the last one again, not used)
 #pragma unroll
         for (int t = 0; t < MT; t++)
             few_left<IN>(x[q][t], rows[t], plane, 32u * b + 8u * g);
+#pragma unroll
+        for (int k = 0; k < NM; k++)
+            few_load<FMT>(w[q][k], data, scale, C, b, at_data[k], at_scale[k]);
     };
 #pragma unroll
-    for (int q = 0; q < DEPTH - 1; q++)
+    for (int q = 0; q < D - 1; q++)
         fetch(q, q);
-    for (uint32_t s = 0; s < n; s += DEPTH)
+    for (uint32_t s = 0; s < n; s += D)
 #pragma unroll
-        for (int q = 0; q < DEPTH; q++) {
-            fetch((q + DEPTH - 1) % DEPTH, s + q + DEPTH - 1);
+        for (int q = 0; q < D; q++) {
+            fetch((q + D - 1) % D, s + q + D - 1);
             __builtin_amdgcn_sched_barrier(0);
             if (s + q < n) {
                 bf16x8_t a[MT][terms];
@@ -342,7 +360,7 @@ __device__ __forceinline__ void few_sums(f32x4_t (&acc)[MT][NM][kFewU], const __
 #pragma unroll
                 for (int k = 0; k < NM; k++)
 #pragma unroll
-                    for (int u = 0; u < kFewU; u++) {
+                    for (int u = 0; u < FewCols<FMT>::lane; u++) {
                         const bf16x8_t b = few_widen<FMT>(w[q][k], u);
 #pragma unroll
                         for (int t = 0; t < MT; t++)
@@ -353,6 +371,20 @@ __device__ __forceinline__ void few_sums(f32x4_t (&acc)[MT][NM][kFewU], const __
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+}
+
+// Two values that a workgroup on another XCD will read in the same launch, and such a read.
+// Each XCD has its own L2; accesses at agent scope go past it.
+__device__ __forceinline__ void store_shared(float *p, float a, float b)
+{
+    const uint64_t v = (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2_t load_shared(const float *p)
+{
+    const uint64_t v =
+        __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return f32x2_t{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
 }
 
 // What a workgroup does with each finished result: stage 1 the activation, stage 2 the
@@ -367,13 +399,14 @@ struct FewOut {
 __device__ __forceinline__ float silu(float z) { return z / (1.0f + __expf(-z)); }
 
 template <int FMT, int IN, int NM, int MT>
-__device__ __forceinline__ void few_tiles(float (*sums)[NM * kFewU * 4][64], const FewRoute &route, uint32_t first,
+__device__ __forceinline__ void few_tiles(float (*sums)[NM * 16][64], uint32_t waves, const FewRoute &route, uint32_t first,
                                           uint32_t count, const FewMatrix &m, uint32_t K, const uint16_t *left,
                                           uint32_t slots, uint64_t plane, uint32_t n0, const FewOut &out)
 {
     const uint32_t tid = threadIdx.x, lane = tid & 63u, i = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     constexpr uint32_t CB = FMT == kOutE2M1 ? 2 : 4;
+    constexpr int U = FewCols<FMT>::lane;
     const __amdgpu_buffer_rsrc_t data =
         __builtin_amdgcn_make_buffer_rsrc((void *)m.data, (short)0, (int)(K / 4u * CB * m.C), kMmBufferFlags);
     const __amdgpu_buffer_rsrc_t scale =
@@ -381,7 +414,7 @@ __device__ __forceinline__ void few_tiles(float (*sums)[NM * kFewU * 4][64], con
     uint32_t at_data[NM], at_scale[NM];
 #pragma unroll
     for (int k = 0; k < NM; k++) {
-        const uint32_t col = n0 + 4u * i, c = col + k * out.cols;
+        const uint32_t col = n0 + U * i, c = col + k * out.cols;
         at_data[k] = col < out.cols ? 2u * g * CB * m.C + CB * c : kDropOffset;
         at_scale[k] = col < out.cols ? c : kDropOffset;
     }
@@ -392,163 +425,218 @@ __device__ __forceinline__ void few_tiles(float (*sums)[NM * kFewU * 4][64], con
         const uint32_t pair = route.pairs[min(first + 16u * t + i, count - 1u)];
         rows[t] = left + (uint64_t)(IN == kInSplit ? pair : pair / slots) * K;
     }
-    f32x4_t acc[MT][NM][kFewU];
+    f32x4_t acc[MT][NM][U];
 #pragma unroll
     for (int t = 0; t < MT; t++)
 #pragma unroll
         for (int k = 0; k < NM; k++)
 #pragma unroll
-            for (int u = 0; u < kFewU; u++)
+            for (int u = 0; u < U; u++)
                 acc[t][k][u] = f32x4_t{};
-    few_sums<FMT, IN, NM, MT>(acc, data, scale, m.C, K / 32u, at_data, at_scale, rows, plane, wave, g);
+    few_sums<FMT, IN, NM, MT>(acc, data, scale, m.C, K / 32u, at_data, at_scale, rows, plane, wave, waves, g);
 
+    // 16 pairs and four of each lane's columns at a time, through LDS
 #pragma unroll
-    for (int t = 0; t < MT; t++) {
+    for (int part = 0; part < MT * U / 4; part++) {
+        const int t = part / (U / 4), u0 = part % (U / 4) * 4;
         if (first + 16u * t >= count)
             break;
-        __syncthreads();     // the last tile's sums have been read
+        __syncthreads();     // the last part's sums have been read
 #pragma unroll
         for (int k = 0; k < NM; k++)
 #pragma unroll
-            for (int u = 0; u < kFewU; u++)
+            for (int u = 0; u < 4; u++)
 #pragma unroll
                 for (int r = 0; r < 4; r++)
-                    sums[wave][(k * kFewU + u) * 4 + r][lane] = acc[t][k][u][r];
+                    sums[wave][(k * 4 + u) * 4 + r][lane] = acc[t][k][u0 + u][r];
         __syncthreads();
-        // 16 rows x 64 columns, two columns a thread
-        const uint32_t row = tid >> 5, c = 2u * (tid & 31u), col = n0 + c;
-        if (first + 16u * t + row >= count || col >= out.cols)
-            continue;
-        const uint32_t pair = route.pairs[first + 16u * t + row];
-        float z[NM][2];
+        // two columns at a time
+        for (uint32_t at = tid; at < 512u; at += 64u * waves) {
+            const uint32_t row = at >> 5, c = 2u * (at & 31u), col = n0 + U * (c >> 2) + u0 + (c & 3u);
+            if (first + 16u * t + row >= count || col >= out.cols)
+                continue;
+            const uint32_t pair = route.pairs[first + 16u * t + row];
+            float z[NM][2];
 #pragma unroll
-        for (int k = 0; k < NM; k++)
+            for (int k = 0; k < NM; k++)
 #pragma unroll
-            for (uint32_t q = 0; q < 2; q++) {
-                const uint32_t reg = (k * kFewU + (c + q) % 4u) * 4u + (row & 3u), l = 16u * (row >> 2) + (c + q) / 4u;
-                float v = sums[0][reg][l];
+                for (uint32_t q = 0; q < 2; q++) {
+                    const uint32_t reg = (k * 4 + (c + q) % 4u) * 4u + (row & 3u);
+                    const uint32_t l = 16u * (row >> 2) + (c + q) / 4u;
+                    float v = 0.0f;
 #pragma unroll
-                for (uint32_t w = 1; w < kFewWaves; w++)
-                    v += sums[w][reg][l];
-                if (!__builtin_isfinite(v))
-                    v = few_exact<FMT, IN>(m.data, m.scale, m.C, col + q + k * out.cols, K,
-                                           left + (uint64_t)(IN == kInSplit ? pair : pair / slots) * K, plane);
-                z[k][q] = v;
+                    for (uint32_t w = 0; w < kFewWaves; w++)
+                        v += w < waves ? sums[min(w, waves - 1u)][reg][l] : 0.0f;
+                    if (!__builtin_isfinite(v))
+                        v = few_exact<FMT, IN>(m.data, m.scale, m.C, col + q + k * out.cols, K,
+                                               left + (uint64_t)(IN == kInSplit ? pair : pair / slots) * K, plane);
+                    z[k][q] = v;
+                }
+            const uint64_t o = (uint64_t)pair * out.cols + col;
+            if constexpr (IN == kInSplit) {
+                store_shared(out.y + o, z[0][0], z[0][1]);
+            } else {
+                float h[2];
+#pragma unroll
+                for (int q = 0; q < 2; q++)
+                    h[q] = NM == 2 ? silu(z[0][q]) * z[NM - 1][q] : silu(z[0][q]);
+                uint32_t high, low;
+                split_pair(h[0], h[1], high, low);
+                *reinterpret_cast<uint32_t *>(out.h + o) = high;
+                *reinterpret_cast<uint32_t *>(out.h + out.plane + o) = low;
             }
-        const uint64_t o = (uint64_t)pair * out.cols + col;
-        if constexpr (IN == kInSplit) {
-            *reinterpret_cast<float2 *>(out.y + o) = float2{z[0][0], z[0][1]};
-        } else {
-            float h[2];
-#pragma unroll
-            for (int q = 0; q < 2; q++)
-                h[q] = NM == 2 ? silu(z[0][q]) * z[NM - 1][q] : silu(z[0][q]);
-            uint32_t high, low;
-            split_pair(h[0], h[1], high, low);
-            *reinterpret_cast<uint32_t *>(out.h + o) = high;
-            *reinterpret_cast<uint32_t *>(out.h + out.plane + o) = low;
         }
     }
 }
 
-template <int FMT, int IN, int NM>
-__device__ __forceinline__ void few_expert(float (*sums)[NM * kFewU * 4][64], const FewRoute &route, uint32_t count,
+// All of the expert's pairs, up to 16 MX at a time.
+template <int FMT, int IN, int NM, int MX>
+__device__ __forceinline__ void few_expert(float (*sums)[NM * 16][64], uint32_t waves, const FewRoute &route, uint32_t count,
                                            const FewMatrix &m, uint32_t K, const uint16_t *left, uint32_t slots,
                                            uint64_t plane, uint32_t n0, const FewOut &out)
 {
-    uint32_t first = 0;
-    for (; count - first > 32u; first += 64u) {
-        few_tiles<FMT, IN, NM, 4>(sums, route, first, count, m, K, left, slots, plane, n0, out);
-        if (count - first <= 64u)
-            return;
+    for (uint32_t first = 0; first < count; first += 16u * MX) {
+        if (MX == 4 && count - first > 32u)
+            few_tiles<FMT, IN, NM, MX>(sums, waves, route, first, count, m, K, left, slots, plane, n0, out);
+        else if (count - first > 16u)
+            few_tiles<FMT, IN, NM, 2>(sums, waves, route, first, count, m, K, left, slots, plane, n0, out);
+        else
+            few_tiles<FMT, IN, NM, 1>(sums, waves, route, first, count, m, K, left, slots, plane, n0, out);
     }
-    if (count - first > 16u)
-        few_tiles<FMT, IN, NM, 2>(sums, route, first, count, m, K, left, slots, plane, n0, out);
-    else
-        few_tiles<FMT, IN, NM, 1>(sums, route, first, count, m, K, left, slots, plane, n0, out);
 }
 
 // ----------------------------------------------------------------------------
-// The two kernels: workgroup (a, tile) has the a-th expert in use and 64 columns
+// The two kernels: a workgroup (of any number of waves up to 8) has an expert in use and 64 or
+// 128 columns
 // ----------------------------------------------------------------------------
 
-template <int FMT, int IN, int ACT, typename ID>
-__global__ __launch_bounds__(kFewThreads) void few_up_kernel(
+extern __shared__ float few_lds[];   // a wave's sums of a part, for each wave
+
+// Waves per SIMD that the registers are to leave room for.
+constexpr int few_room(int fmt, int NM, int MX) { return MX == 4 || NM == 2 ? 2 : fmt == kOutE2M1 ? 3 : 4; }
+
+template <int FMT, int IN, int ACT, int MX, typename ID>
+__global__ __launch_bounds__(kFewThreads, few_room(FMT, ACT == kActSwiglu ? 2 : 1, MX)) void few_up_kernel(
     const uint16_t *__restrict__ x, uint32_t K, const void *__restrict__ ids, uint32_t pairs, uint32_t slots,
     uint32_t experts, const uint8_t *__restrict__ w, const uint8_t *__restrict__ w_scale, uint32_t F, uint32_t tiles,
-    uint16_t *__restrict__ h, uint32_t *__restrict__ arrived, uint32_t arrivals)
+    uint16_t *__restrict__ h, uint32_t *__restrict__ arrived, uint32_t down_tiles, uint16_t *__restrict__ out_rows,
+    uint32_t N)
 {
     constexpr int NM = ACT == kActSwiglu ? 2 : 1;
     constexpr uint32_t CB = FMT == kOutE2M1 ? 2 : 4;
     __shared__ FewRoute route;
-    __shared__ float sums[kFewWaves][NM * kFewU * 4][64];
-    const uint32_t a = blockIdx.x / tiles, tile = blockIdx.x - a * tiles;
-    // the second kernel's counters
-    if (blockIdx.x == 0)
-        for (uint32_t k = threadIdx.x; k < arrivals; k += kFewThreads)
-            arrived[k] = 0;
-    uint32_t expert, count, active;
-    if (!few_route<ID>(route, ids, pairs, experts, a, expert, count, active))
-        return;
-    const uint32_t C = NM * F;
-    const FewMatrix m = {w + (uint64_t)expert * (K / 4u) * CB * C, w_scale + (uint64_t)expert * (K / 32u) * C, C};
-    const FewOut out = {h, nullptr, (uint64_t)pairs * F, F};
-    few_expert<FMT, IN, NM>(sums, route, count, m, K, x, slots, 0, tile * kFewCols, out);
+    // (e2m1's gated sums of 64 pairs do not fit the registers)
+    constexpr int MT = NM == 2 && FMT == kOutE2M1 ? 2 : MX;
+    const auto sums = reinterpret_cast<float(*)[NM * 16][64]>(few_lds);
+    FewPlace at;
+    if (few_route<ID>(route, ids, pairs, experts, tiles, at)) {
+        const uint32_t C = NM * F;
+        const FewMatrix m = {w + (uint64_t)at.expert * (K / 4u) * CB * C,
+                             w_scale + (uint64_t)at.expert * (K / 32u) * C, C};
+        const FewOut out = {h, nullptr, (uint64_t)pairs * F, F};
+        few_expert<FMT, IN, NM, MT>(sums, blockDim.x / 64u, route, at.count, m, K, x, slots, 0, at.tile * FewCols<FMT>::all,
+                                    out);
+    }
+    // for the second kernel: each token's count of pairs that have an expert, up to zero in
+    // every column tile; a token without any gets its zeros
+    const uint32_t lane = threadIdx.x & 63u, tokens = pairs / slots;
+    for (uint32_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+        const ID e = reinterpret_cast<const ID *>(ids)[t * slots + min(lane, slots - 1u)];
+        const uint32_t has =
+            (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(lane < slots && e >= 0 && (uint64_t)e < experts));
+        for (uint32_t k = threadIdx.x; k < down_tiles; k += blockDim.x)
+            arrived[k * tokens + t] = 0u - has;
+        if (has == 0)
+            for (uint32_t c = 4u * threadIdx.x; c < N; c += 4u * blockDim.x)
+                *reinterpret_cast<u32x2_t *>(out_rows + (uint64_t)t * N + c) = u32x2_t{0u, 0u};
+    }
 }
 
-// The workgroup that is the last of its columns' adds up the pairs' rows in slot
-// order. Arrivals only say that the others' rows are written; the sums do not depend on
-// their order.
-template <int FMT, int IN, typename ID>
-__global__ __launch_bounds__(kFewThreads) void few_down_kernel(
+// A workgroup that has written its columns of its pairs' rows of y says so for each pair's
+// token, and adds up the slots of the tokens that are complete with that, in slot order:
+// the sums do not depend on the order of arrival. Rows are written and read past the L2s
+// (store_shared), so an arrival only has to come after a wave's own stores, which each wave
+// waits for before the barrier in front of it. With ordinary stores and a fence on either
+// side, which writes back and drops whole L2s, this kernel took 440 us instead of 44 (16 x
+// 4 pairs, 32 experts of e4m3fn, 2048 x 4096).
+template <int FMT, int IN, int MX, typename ID>
+__global__ __launch_bounds__(kFewThreads, few_room(FMT, 1, MX)) void few_down_kernel(
     const uint16_t *__restrict__ h, uint32_t F, const void *__restrict__ ids, uint32_t pairs, uint32_t slots,
     uint32_t experts, const uint8_t *__restrict__ w, const uint8_t *__restrict__ w_scale, uint32_t N, uint32_t tiles,
     float *y, uint32_t *arrived, const float *__restrict__ weights, uint16_t *__restrict__ out)
 {
     constexpr uint32_t CB = FMT == kOutE2M1 ? 2 : 4;
     __shared__ FewRoute route;
-    __shared__ float sums[kFewWaves][kFewU * 4][64];
-    __shared__ uint32_t last;
-    const uint32_t a = blockIdx.x / tiles, tile = blockIdx.x - a * tiles;
-    const uint32_t n0 = tile * kFewCols;
-    uint32_t expert, count, active = 0;
-    if (few_route<ID>(route, ids, pairs, experts, a, expert, count, active)) {
-        const FewMatrix m = {w + (uint64_t)expert * (F / 4u) * CB * N, w_scale + (uint64_t)expert * (F / 32u) * N, N};
-        const FewOut o = {nullptr, y, 0, N};
-        few_expert<FMT, kInSplit, 1>(sums, route, count, m, F, h, slots, (uint64_t)pairs * F, n0, o);
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0)
-            last = atomicAdd(&arrived[tile], 1u) == active - 1u ? 1u : 0u;
-        __syncthreads();
-        if (!last)
-            return;
-        __threadfence();
-    } else if (a > 0 || active > 0) {
+    __shared__ uint32_t complete;
+    const auto sums = reinterpret_cast<float(*)[16][64]>(few_lds);
+    FewPlace at;
+    if (!few_route<ID>(route, ids, pairs, experts, tiles, at))
         return;
-    }
-    // (no expert in use: the first workgroup of the columns writes zeros)
+    const uint32_t n0 = at.tile * FewCols<FMT>::all;
+    const FewMatrix m = {w + (uint64_t)at.expert * (F / 4u) * CB * N, w_scale + (uint64_t)at.expert * (F / 32u) * N, N};
+    const FewOut o = {nullptr, y, 0, N};
+    few_expert<FMT, kInSplit, 1, MX>(sums, blockDim.x / 64u, route, at.count, m, F, h, slots, (uint64_t)pairs * F, n0,
+                                     o);
     const ID *id = reinterpret_cast<const ID *>(ids);
-    const uint32_t tokens = pairs / slots;
-    for (uint32_t q = threadIdx.x; q < tokens * (kFewCols / 2u); q += kFewThreads) {
-        const uint32_t t = q / (kFewCols / 2u), col = n0 + 2u * (q % (kFewCols / 2u));
-        if (col >= N)
-            continue;
-        float sum[2] = {0.0f, 0.0f};
-        for (uint32_t j = 0; j < slots; j++) {
-            const uint32_t p = t * slots + j;
-            if (id[p] >= 0 && (uint64_t)id[p] < experts) {
-                const float2 v = *reinterpret_cast<const float2 *>(y + (uint64_t)p * N + col);
-                sum[0] = __builtin_fmaf(weights[p], v.x, sum[0]);
-                sum[1] = __builtin_fmaf(weights[p], v.y, sum[1]);
-            }
+    if (threadIdx.x == 0)
+        complete = 0;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    for (uint32_t k = threadIdx.x; k < at.count; k += blockDim.x) {
+        const uint32_t t = route.pairs[k] / slots;
+        const uint32_t before = __hip_atomic_fetch_add(&arrived[at.tile * (pairs / slots) + t], 1u, __ATOMIC_RELAXED,
+                                                       __HIP_MEMORY_SCOPE_AGENT);
+        if (before + 1u == 0u)       // (the sums have been read: their memory holds the list)
+            reinterpret_cast<uint16_t *>(few_lds)[atomicAdd(&complete, 1u)] = (uint16_t)t;
+    }
+    __syncthreads();
+    const uint32_t tokens = complete;
+    // two columns of two of them at a time, and eight slots' reads of each (one by one, each
+    // read waits for the one before)
+    constexpr uint32_t half = FewCols<FMT>::all / 2u;
+    const uint32_t items = tokens * half;
+    for (uint32_t q0 = threadIdx.x; q0 < items; q0 += 2u * blockDim.x) {
+        uint32_t t[2], col[2];
+        float sum[2][2] = {};
+#pragma unroll
+        for (uint32_t k = 0; k < 2; k++) {
+            const uint32_t q = min(q0 + k * blockDim.x, items - 1u);
+            t[k] = reinterpret_cast<const uint16_t *>(few_lds)[q / half];
+            col[k] = min(n0 + 2u * (q % half), N - 2u);
         }
-        uint32_t bits;
-        if constexpr (IN == kInBF16)
-            bits = bf16_pair(sum[0], sum[1]);
-        else
-            bits = __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)sum[0], (_Float16)sum[1]});
-        *reinterpret_cast<uint32_t *>(out + (uint64_t)t * N + col) = bits;
+        for (uint32_t j0 = 0; j0 < slots; j0 += 8u) {
+            f32x2_t v[2][8];
+            float wt[2][8];
+            bool in[2][8];
+#pragma unroll
+            for (uint32_t k = 0; k < 2; k++)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; j++) {
+                    const uint32_t p = t[k] * slots + min(j0 + j, slots - 1u);
+                    const ID e = id[p];
+                    in[k][j] = j0 + j < slots && e >= 0 && (uint64_t)e < experts;
+                    wt[k][j] = weights[p];
+                    v[k][j] = load_shared(y + (uint64_t)p * N + col[k]);
+                }
+#pragma unroll
+            for (uint32_t k = 0; k < 2; k++)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; j++)
+                    if (in[k][j]) {
+                        sum[k][0] = __builtin_fmaf(wt[k][j], v[k][j].x, sum[k][0]);
+                        sum[k][1] = __builtin_fmaf(wt[k][j], v[k][j].y, sum[k][1]);
+                    }
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 2; k++) {
+            // (an item past the last repeats it, a column past the last the last two)
+            uint32_t bits;
+            if constexpr (IN == kInBF16)
+                bits = bf16_pair(sum[k][0], sum[k][1]);
+            else
+                bits = __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)sum[k][0], (_Float16)sum[k][1]});
+            *reinterpret_cast<uint32_t *>(out + (uint64_t)t[k] * N + col[k]) = bits;
+        }
     }
 }
 
