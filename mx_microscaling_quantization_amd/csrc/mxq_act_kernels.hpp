@@ -18,6 +18,13 @@
 // neighbouring lanes' (two quad permutes), one down a column four lanes' 16 apart
 // (two lane swaps). The rounded values go through the quantize's own helpers
 // (mxq_quantize_kernels.hpp), so the bytes are those of quantizing them by themselves.
+//
+// Memory bounds both passes (bf16, e4m3fn, swiglu of 16384 x 4096: forward 84 us, 5.7 TB/s;
+// backward 111 us, 5.5 TB/s). What costs is the layout of the codes along the rows: 128
+// bytes of each view row for a tile. In the backward pass the arithmetic (some 45
+// instructions for each of the tile's values) takes as long as the memory at its peak, under
+// which it hides: with the five instructions that mend four overflow codes left to a
+// mode of the conversions it took no less.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -58,15 +65,34 @@ __device__ __forceinline__ float sigmoid(float z)
 // A thread's 8 rows x 8 columns as pairs of columns.
 typedef uint32_t ActBlock[8][4];
 
+// Two halves of 16 bytes each of what a lane has to write: swapped between the wave's
+// halves so that lanes l and l + 32 have the two of lane l (x), then of lane l + 32 (y).
+// Stored like that an instruction writes whole runs of memory; a lane's own halves one
+// after the other left every other 16 bytes of them to the next one (backward, silu, 16384
+// x 4096: 74 us, 70 so; swiglu in f16, 16384 x 1408: 47.5 and 44.4).
+__device__ __forceinline__ void act_swap(u32x4_t &x, u32x4_t &y)
+{
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const uint32_t a = x[k], b = y[k];
+        const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+        x[k] = r[0];
+        y[k] = r[1];
+    }
+}
+
 // ---- along the rows ----------------------------------------------------------------
 
 // Codes and scales of the rows' blocks of 32: containers of view rows p0 and p0 + 1 (the
-// thread's columns), rows row0 .. row0 + 7, of a [., R] view.
+// thread's columns), rows row0 .. row0 + 7, of a [., R] view. whole: all 32 rows of the wave
+// are there.
 template <int IN, int OUT>
 __device__ __forceinline__ void act_along(const ActBlock &w, int emax, uint64_t R, uint32_t row0, uint32_t p0,
-                                          uint32_t lane, uint8_t *__restrict__ data, uint8_t *__restrict__ scale)
+                                          uint32_t lane, bool whole, uint8_t *__restrict__ data,
+                                          uint8_t *__restrict__ scale)
 {
     uint32_t e[8], code[2][8];
+    bool special = false;
 #pragma unroll
     for (int r = 0; r < 8; r += 2) {
         uint32_t m[2];
@@ -82,22 +108,25 @@ __device__ __forceinline__ void act_along(const ActBlock &w, int emax, uint64_t 
 #pragma unroll
         for (int q = 0; q < 2; q++) {
             const uint32_t mag = half16(v, q);
+            special |= mag > InfBits<IN>::value;
             e[r + q] = block_e8m0<IN>(mag, emax);
             const float s = e8m0_to_scale(e[r + q]);
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 const uint32_t *x = &w[r + q][2 * j];
-                uint32_t c[1];
                 if constexpr (OUT == kOutE2M1)
-                    c[0] = fp4_container<IN, 0>(0u, x[0], x[1], s);
+                    code[j][r + q] = fp4_container<IN, 0>(0u, x[0], x[1], s);
                 else
-                    c[0] = fp8x4<IN, OUT>(x[0], x[1], s);
-                if (mag > InfBits<IN>::value)
-                    fix_special_codes<IN, OUT, 1>(x, &e[r + q], c);
-                code[j][r + q] = c[0];
+                    code[j][r + q] = fp8x4<IN, OUT>(x[0], x[1], s);
             }
         }
     }
+    if (special)    // (one branch for all: sixteen kept the compiler from ordering anything)
+#pragma unroll
+        for (int r = 0; r < 8; r++)
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                fix_special_codes<IN, OUT, 1>(&w[r][2 * j], &e[r], &code[j][r]);
 #pragma unroll
     for (int j = 0; j < 2; j++) {
         const uint64_t at = (uint64_t)(p0 + j) * R + row0;
@@ -108,9 +137,17 @@ __device__ __forceinline__ void act_along(const ActBlock &w, int emax, uint64_t 
                 v[k] = (code[j][2 * k] & 0xFFFFu) | code[j][2 * k + 1] << 16;
             *reinterpret_cast<u32x4_t *>(data + 2u * at) = v;
         } else {
-            u32x4_t *p = reinterpret_cast<u32x4_t *>(data + 4u * at);
-            p[0] = u32x4_t{code[j][0], code[j][1], code[j][2], code[j][3]};
-            p[1] = u32x4_t{code[j][4], code[j][5], code[j][6], code[j][7]};
+            u32x4_t x = {code[j][0], code[j][1], code[j][2], code[j][3]};
+            u32x4_t y = {code[j][4], code[j][5], code[j][6], code[j][7]};
+            uint8_t *p = data + 4u * at;
+            uint32_t next = 16u;
+            if (whole) {     // 64 bytes of lanes 16 apart in each store
+                act_swap(x, y);
+                p = p - 32u * (lane >> 4) + 32u * ((lane >> 4) & 1u) + 16u * (lane >> 5);
+                next = 64u;
+            }
+            *reinterpret_cast<u32x4_t *>(p) = x;
+            *reinterpret_cast<u32x4_t *>(p + next) = y;
         }
     }
     if ((lane & 3u) == 0)
@@ -127,6 +164,13 @@ __device__ __forceinline__ void act_down(const ActBlock &w, int emax, uint64_t C
                                          uint32_t lane, uint8_t *__restrict__ data, uint8_t *__restrict__ scale)
 {
     uint32_t e[8], code[2][8];
+    bool special = false;
+    // rows 4 j .. 4 j + 3 of column 2 k + q
+    const auto column = [&](int j, int k, int q, uint32_t (&x)[2]) {
+        const uint32_t pick = q ? 0x07060302u : 0x05040100u;
+        x[0] = __builtin_amdgcn_perm(w[4 * j + 1][k], w[4 * j][k], pick);
+        x[1] = __builtin_amdgcn_perm(w[4 * j + 3][k], w[4 * j + 2][k], pick);
+    };
 #pragma unroll
     for (int k = 0; k < 4; k++) {
         uint32_t v = 0;
@@ -141,24 +185,29 @@ __device__ __forceinline__ void act_down(const ActBlock &w, int emax, uint64_t C
 #pragma unroll
         for (int q = 0; q < 2; q++) {
             const uint32_t mag = half16(v, q);
+            special |= mag > InfBits<IN>::value;
             e[2 * k + q] = block_e8m0<IN>(mag, emax);
             const float s = e8m0_to_scale(e[2 * k + q]);
-            const uint32_t pick = q ? 0x07060302u : 0x05040100u;
 #pragma unroll
             for (int j = 0; j < 2; j++) {
-                const uint32_t x[2] = {__builtin_amdgcn_perm(w[4 * j + 1][k], w[4 * j][k], pick),
-                                       __builtin_amdgcn_perm(w[4 * j + 3][k], w[4 * j + 2][k], pick)};
-                uint32_t c[1];
+                uint32_t x[2];
+                column(j, k, q, x);
                 if constexpr (OUT == kOutE2M1)
-                    c[0] = fp4_container<IN, 0>(0u, x[0], x[1], s);
+                    code[j][2 * k + q] = fp4_container<IN, 0>(0u, x[0], x[1], s);
                 else
-                    c[0] = fp8x4<IN, OUT>(x[0], x[1], s);
-                if (mag > InfBits<IN>::value)
-                    fix_special_codes<IN, OUT, 1>(x, &e[2 * k + q], c);
-                code[j][2 * k + q] = c[0];
+                    code[j][2 * k + q] = fp8x4<IN, OUT>(x[0], x[1], s);
             }
         }
     }
+    if (special)
+#pragma unroll
+        for (int c = 0; c < 8; c++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                uint32_t x[2];
+                column(j, c >> 1, c & 1, x);
+                fix_special_codes<IN, OUT, 1>(x, &e[c], &code[j][c]);
+            }
 #pragma unroll
     for (int j = 0; j < 2; j++) {
         const uint64_t at = (uint64_t)(row0 / 4u + j) * C + col;
@@ -169,9 +218,16 @@ __device__ __forceinline__ void act_down(const ActBlock &w, int emax, uint64_t C
                 v[k] = (code[j][2 * k] & 0xFFFFu) | code[j][2 * k + 1] << 16;
             *reinterpret_cast<u32x4_t *>(data + 2u * at) = v;
         } else {
-            u32x4_t *p = reinterpret_cast<u32x4_t *>(data + 4u * at);
-            p[0] = u32x4_t{code[j][0], code[j][1], code[j][2], code[j][3]};
-            p[1] = u32x4_t{code[j][4], code[j][5], code[j][6], code[j][7]};
+            u32x4_t x = {code[j][0], code[j][1], code[j][2], code[j][3]};
+            u32x4_t y = {code[j][4], code[j][5], code[j][6], code[j][7]};
+            act_swap(x, y);
+            // rows of lanes 0 .. 31, then of lanes 32 .. 63 (16 rows of the tensor on)
+            uint8_t *p = data + 4u * at + (lane >> 5) * 16u - (lane >> 5) * 16u * C;
+            // past the caches, whole lines as they are (backward, swiglu, 16384 x 4096: 138 -> 111
+            // us; the 64 bytes of a line that act_along writes at a time are not: 113 with
+            // the hint there alone, 133 with it everywhere)
+            __builtin_nontemporal_store(x, reinterpret_cast<u32x4_t *>(p));
+            __builtin_nontemporal_store(y, reinterpret_cast<u32x4_t *>(p + 16u * C));
         }
     }
     if (lane < 16u)
@@ -188,6 +244,7 @@ __device__ __forceinline__ void act_keep(const ActBlock &w, int emax, uint64_t W
 {
     uint32_t e[2];
     uint32_t code[8][2];
+    bool special = false;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
         uint32_t v = 0;
@@ -195,16 +252,17 @@ __device__ __forceinline__ void act_keep(const ActBlock &w, int emax, uint64_t W
         for (int r = 0; r < 8; r++)
             v = pk_max_u16(v, pk_max_u16(w[r][2 * j] & 0x7FFF7FFFu, w[r][2 * j + 1] & 0x7FFF7FFFu));
         const uint32_t mag = max(v & 0xFFFFu, v >> 16);
+        special |= mag > InfBits<IN>::value;
         e[j] = block_e8m0<IN>(mag, emax);
         const float s = e8m0_to_scale(e[j]);
 #pragma unroll
-        for (int r = 0; r < 8; r++) {
-            uint32_t c[1] = {fp8x4<IN, OUT>(w[r][2 * j], w[r][2 * j + 1], s)};
-            if (mag > InfBits<IN>::value)
-                fix_special_codes<IN, OUT, 1>(&w[r][2 * j], &e[j], c);
-            code[r][j] = c[0];
-        }
+        for (int r = 0; r < 8; r++)
+            code[r][j] = fp8x4<IN, OUT>(w[r][2 * j], w[r][2 * j + 1], s);
     }
+    if (special)
+#pragma unroll
+        for (int r = 0; r < 8; r++)
+            fix_special_codes<IN, OUT, 2>(w[r], e, code[r]);
 #pragma unroll
     for (int r = 0; r < 8; r++)
         *reinterpret_cast<u32x2_t *>(data + (row0 + r) * W + col) = u32x2_t{code[r][0], code[r][1]};
@@ -252,12 +310,14 @@ __device__ __forceinline__ bool act_scales(uint32_t bytes, float (&s)[2])
 // Workgroup (a wave) -> tile of 32 rows x 128 columns.
 struct ActTile {
     uint32_t row0, col;
+    bool whole;     // 32 rows
 };
-__device__ __forceinline__ ActTile act_tile(uint32_t tiles_c)
+__device__ __forceinline__ ActTile act_tile(uint32_t R, uint32_t tiles_c)
 {
     const uint32_t t = tile_index<kMmXcds>();
     const uint32_t band = t / tiles_c, lane = threadIdx.x;
-    return ActTile{band * kActRows + 8u * (lane >> 4), (t - band * tiles_c) * kActCols + 8u * (lane & 15u)};
+    return ActTile{band * kActRows + 8u * (lane >> 4), (t - band * tiles_c) * kActCols + 8u * (lane & 15u),
+                   band * kActRows + kActRows <= R};
 }
 
 // R a multiple of 8, F of 32: whole lanes of a quad are in or out.
@@ -269,7 +329,7 @@ __global__ __launch_bounds__(64) void act_quantize_kernel(const uint16_t *__rest
                                                           uint8_t *__restrict__ saved_scale)
 {
     constexpr int NM = ACT == kActSwiglu ? 2 : 1;
-    const ActTile t = act_tile(tiles_c);
+    const ActTile t = act_tile(R, tiles_c);
     if (t.row0 >= R || t.col >= F)
         return;
     const uint64_t W = (uint64_t)NM * F;
@@ -301,7 +361,7 @@ __global__ __launch_bounds__(64) void act_quantize_kernel(const uint16_t *__rest
             }
             h[r][c] = pack16<IN>(a, b);
         }
-    act_along<IN, OUT>(h, emax, R, t.row0, t.col / 4u, threadIdx.x, data, scale);
+    act_along<IN, OUT>(h, emax, R, t.row0, t.col / 4u, threadIdx.x, t.whole, data, scale);
 }
 
 // R and F multiples of 32.
@@ -313,7 +373,7 @@ __global__ __launch_bounds__(64, 2) void act_backward_kernel(
     uint8_t *__restrict__ h_data, uint8_t *__restrict__ h_scale)
 {
     constexpr int NM = ACT == kActSwiglu ? 2 : 1;
-    const ActTile t = act_tile(tiles_c);
+    const ActTile t = act_tile(R, tiles_c);
     if (t.col >= F)
         return;
     const uint64_t W = (uint64_t)NM * F;
@@ -333,19 +393,20 @@ __global__ __launch_bounds__(64, 2) void act_backward_kernel(
     for (int k = 0; k < NM; k++)
         sb[k] = *reinterpret_cast<const uint16_t *>(saved_scale + (t.row0 / 8u) * (W / 4u) + (k * F + t.col) / 4u);
     float s[NM][2];
-    bool twice[NM];
+    bool twice = false;
 #pragma unroll
     for (int k = 0; k < NM; k++)
-        twice[k] = act_scales(sb[k], s[k]);
+        twice |= act_scales(sb[k], s[k]);
 
     ActBlock dz[NM], h;
 #pragma unroll
     for (int r = 0; r < 8; r++) {
+        __builtin_amdgcn_sched_barrier(0);
         float v[NM][8];
 #pragma unroll
         for (int k = 0; k < NM; k++) {
             act_decode<SV>(code[k][r], s[k], v[k]);
-            if (twice[k])
+            if (twice)
 #pragma unroll
                 for (int c = 0; c < 8; c++)
                     v[k][c] *= ((sb[k] >> (8 * (c >> 2))) & 0xFFu) == 255u ? 2.0f : 1.0f;
@@ -374,12 +435,28 @@ __global__ __launch_bounds__(64, 2) void act_backward_kernel(
             for (int k = 0; k < NM; k++)
                 dz[k][r][c] = pack16<IN>(out[k][0], out[k][1]);
             h[r][c] = pack16<IN>(out[NM][0], out[NM][1]);
+            // (rounded here, not where it is first used: a word instead of its operands)
+#pragma unroll
+            for (int k = 0; k < NM; k++)
+                asm volatile("" : "+v"(dz[k][r][c]));
+            asm volatile("" : "+v"(h[r][c]));
         }
     }
+    // one after the other: mixed, their temporaries fill the registers, as do the masked
+    // values that two of them would share
+    __builtin_amdgcn_sched_barrier(0);
     act_down<IN, OUT>(h, emax, F, t.row0, t.col, threadIdx.x, h_data, h_scale);
 #pragma unroll
     for (int k = 0; k < NM; k++) {
-        act_along<IN, OUT>(dz[k], emax, R, t.row0, (k * F + t.col) / 4u, threadIdx.x, rows_data, rows_scale);
+        __builtin_amdgcn_sched_barrier(0);
+        act_along<IN, OUT>(dz[k], emax, R, t.row0, (k * F + t.col) / 4u, threadIdx.x, true, rows_data,
+                           rows_scale);
+#pragma unroll
+        for (int r = 0; r < 8; r++)
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+                asm volatile("" : "+v"(dz[k][r][c]));
+        __builtin_amdgcn_sched_barrier(0);
         act_down<IN, OUT>(dz[k], emax, W, t.row0, k * F + t.col, threadIdx.x, cols_data, cols_scale);
     }
 }
