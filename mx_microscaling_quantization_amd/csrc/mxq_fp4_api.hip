@@ -15,14 +15,14 @@ using mxq_host::grid_fits;
 typedef void (*fp4_fn)(const uint8_t *, const uint8_t *, const uint8_t *, const uint8_t *, const int32_t *, uint32_t,
                        uint32_t, uint32_t, uint32_t, uint32_t, uint32_t, void *);
 
-enum { kTile256 = 0, kTile128 = 1, kStreamWide = 2, kStreamNarrow = 3 };
+enum { kTile256 = 0, kTile128 = 1, kStreamWide = 2, kStream = 3, kStreamNarrow = 4 };
 
 // Rows, columns and threads of each form's tile.
 struct Form {
     int64_t rows, cols;
     uint32_t threads;
 };
-constexpr Form kForms[] = {{256, 256, 256}, {128, 128, 256}, {32, 256, 256}, {32, 64, 512}};
+constexpr Form kForms[] = {{256, 256, 256}, {128, 128, 256}, {32, 256, 256}, {32, 128, 256}, {32, 64, 512}};
 
 template <int LF, int EPI> fp4_fn pick_form(int form)
 {
@@ -30,6 +30,7 @@ template <int LF, int EPI> fp4_fn pick_form(int form)
     case kTile256: return mxq::fp4_tile_kernel<LF, EPI, 4>;
     case kTile128: return mxq::fp4_tile_kernel<LF, EPI, 2>;
     case kStreamWide: return mxq::fp4_stream_kernel<LF, EPI, 4, 2, 2>;
+    case kStream: return mxq::fp4_stream_kernel<LF, EPI, 4, 1, 4>;
     default: return mxq::fp4_stream_kernel<LF, EPI, 2, 1, 8>;
     }
 }
@@ -70,23 +71,47 @@ int run(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs
          (uintptr_t)offsets) & 15u)
         return MXQ_E_ALIGN;
 
+    // The form follows from the number of tiles: the streams' smallest tiles of which there is
+    // at most one for each of the 256 CUs share a contraction among the most waves and CUs.
+    // From 128-row tiles on two fit a CU, and 256-row tiles, with half the copies per product,
+    // win where there are enough of them (us, one group, e4m3fn by e2m1; in brackets e2m1 by
+    // e2m1; narrow: 32 x 64, stream: 32 x 128, wide: 32 x 256):
+    //   M x K x N             narrow  stream  wide      128 x 128    256 x 256
+    //   16 x 4096 x 4096         9.5    12.8  21.1
+    //   128 x 4096 x 4096        9.9    11.5  18.1 (17) 20.3 (13.1)  53.7 (33.6)
+    //   256 x 4096 x 4096       18.7    15.0  18.5
+    //   512 x 4096 x 4096       35.2    22.9  18.7 (18) 20.7 (13.6)  55.2 (34.3)
+    //   2048 x 4096 x 4096                    55 (53)   32.9 (23.4)  57.6 (36.5)
+    //   16 x 8192 x 8192        15.8    20.7  35.1
+    //   256 x 8192 x 8192                     44 (44)   37.5 (23.3)  102 (60.5)
+    //   256 x 4096 x 14336                    41 (40)   21.3 (15.0)  55.6 (35.2)
+    //   1024 x 4096 x 14336                  140 (140)  57.3 (41.5)  58.0 (38.8)
+    //   2048 x 8192 x 8192                   314 (312)  113 (81.9)   109 (70.7)
+    // Groups of up to 64 rows stream their weights whatever their number (64 x 64 rows, 4096 x
+    // 2048: wide 74 (72), 128 x 128 84 (68)). A group's last tile is filled in part, half of
+    // it on average, so 256-row tiles need the rows to make up for it (64 even groups, 4096 x
+    // 2048, 256 x 256 against 128 x 128: 128 rows 137 (94), 101 (81); 256 rows 146 (99), 156
+    // (118); 512 rows 277 (192), 276 (209)), and a short contraction is mostly the stores of
+    // its results, which two tiles on a CU overlap.
     const int64_t mean = M / groups, kCus = 256;
-    const auto tiles = [&](int form, int64_t rows) {
+    const auto tiles = [&](int form) {
         const Form &f = kForms[form];
-        return ((rows + f.rows - 1) / f.rows) * ((N + f.cols - 1) / f.cols);
+        return ((M + f.rows - 1) / f.rows) * ((N + f.cols - 1) / f.cols);
     };
     int form;
-    if (mean <= 64 || 2 * tiles(kTile128, M) <= kCus)
+    if (tiles(kStreamNarrow) <= kCus)
+        form = kStreamNarrow;
+    else if (tiles(kStream) <= kCus)
+        form = kStream;
+    else if (mean <= 64)
         form = kStreamWide;
-    else if (mean <= 384 || P <= 256)
+    else if (tiles(kTile128) <= 2 * kCus || mean <= (lhs_fmt == MXQ_OUT_E2M1 ? 255 : 383) || P <= 256)
         form = kTile128;
     else
         form = kTile256;
     // the square tiles copy 16 bytes of containers and 4 scale bytes at a time
     if (M % 4 != 0 && form <= kTile128)
         form = kStreamWide;
-    if (form == kStreamWide && 2 * tiles(kStreamWide, M) <= kCus)
-        form = kStreamNarrow;
 
     const Form &f = kForms[form];
     const int64_t tiles_n = (N + f.cols - 1) / f.cols;

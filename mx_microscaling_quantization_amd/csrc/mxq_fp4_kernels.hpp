@@ -261,6 +261,10 @@ __device__ __attribute__((noinline)) void fp4_rare_part(const uint8_t *lhs, cons
 // columns; KW waves share the K steps of a set of columns and add their sums
 // through LDS in wave order. A row of 32 lanes reads 64 U contiguous bytes; 16-bit
 // containers of two rows are put side by side by one byte permute per register.
+//
+// Bound by the weights' bytes with many groups (64 groups of 32 rows, 4096 x 2048, e4m3fn:
+// 51 us, 5.9 TB/s), and by the latency of a launch and of the first loads for one small
+// product (16 x 4096 x 4096: 9.5 us with 32 x 64 tiles of eight waves, 21 with 32 x 256).
 
 // K steps s0 .. s1 - 1, kFp4Ahead of them in flight.
 constexpr int kFp4Ahead = 3;
@@ -400,6 +404,12 @@ __global__ __launch_bounds__(64 * CW * KW, 2) void fp4_stream_kernel(
 //
 // The weights are the A operand, so that a lane holds four adjacent columns of
 // one result row; the results go through LDS once to leave in whole lines.
+//
+// Operands of a step are read while the products before it run, each wave's reads spread
+// over its products, and copies are two or more stages ahead, so that one barrier a stage is
+// all that waits. 8192 x 8192 x 8192 takes 279 us in e2m1 by e2m1 (3.94 PFLOP/s; 297 with the
+// reads bunched) and 421 us in e4m3fn by e2m1 (2.61 PFLOP/s): with FP8 the matrix
+// instructions take twice as long, and an operand 8 LDS reads in place of 4.
 
 constexpr int kTileThreads = 256;
 constexpr uint32_t kTileRows = 32;   // operand rows per stage
@@ -438,10 +448,10 @@ __device__ __forceinline__ void tile_copy_rows(const MmSource &s, uint8_t *dst, 
                                                uint32_t lane)
 {
     constexpr uint32_t per = 1024u / ROW, lanes = ROW / 16u;   // rows per copy, lanes per row
+    // (past the operand the range is empty, whatever the address)
     const uint32_t p0 = row0 + 8u * w;
-    const bool in = p0 < P;
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(s.data + (in ? (uint64_t)p0 * s.pitch : 0ull)), (short)0, in ? (int)(8u * s.pitch - s.col_bytes) : 0,
+        (void *)(s.data + (uint64_t)p0 * s.pitch), (short)0, p0 < P ? (int)(8u * s.pitch - s.col_bytes) : 0,
         kMmBufferFlags);
     const uint32_t row = lane / lanes, at = lane % lanes;
 #pragma unroll
@@ -459,17 +469,22 @@ __device__ __forceinline__ void tile_copy_scale(const MmSource &s, uint8_t *dst,
                                                 uint32_t dense, uint32_t u, uint32_t lane)
 {
     constexpr uint32_t per = 256u / T, lanes = T / 4u;
-    const bool in = block < P / 8u;
-    const uint32_t n = in ? min(P / 8u - block, 4u) : 0u;
+    // (all uniform; said so, or the address is built in vector registers)
+    const uint32_t blocks = P / 8u, left = block < blocks ? blocks - block : 0u;
+    const uint32_t bytes = left > 0u ? min(left, 4u) * s.C - (s.C - s.scale_cols) : 0u;
+    const uint64_t at = scale_row(block, dense) * s.C;
+    const uint64_t p = (uint64_t)(uintptr_t)s.scale + at;
+    const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)p);
+    const uint32_t high = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(s.scale + (in ? scale_row(block, dense) * s.C : 0ull)), (short)0,
-        in ? (int)(n * s.C - (s.C - s.scale_cols)) : 0, kMmBufferFlags);
+        (void *)(uintptr_t)((uint64_t)high << 32 | low), (short)0, (int)__builtin_amdgcn_readfirstlane(bytes),
+        kMmBufferFlags);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)(dst + 256u * u), 4,
                                              (lane / lanes) * s.C + 4u * (lane % lanes), per * u * s.C, 0, 0);
 }
 
 template <int LF, int FR>
-__device__ __forceinline__ void tile_copy(const MmSource &sl, const MmSource &sr, uint8_t *st, uint32_t P,
+__device__ __forceinline__ void tile_copy(const MmSource &sl, const MmSource &sr, uint8_t *__restrict__ st, uint32_t P,
                                           uint32_t stage, uint32_t dense, uint32_t w, uint32_t lane)
 {
     typedef TileLayout<LF, FR> L;
@@ -541,6 +556,56 @@ __device__ __forceinline__ i32x8_t tile_read(const uint8_t *p, uint32_t t)
     }
 }
 
+// A K step's operands, and a stage's scales. (The stage pointers here and in tile_copy are
+// restrict: without that the compiler takes a read for one of what a copy in flight
+// writes, and waits for all copies in front of it.)
+template <int LF, int FR>
+__device__ __forceinline__ void tile_read_step(const uint8_t *__restrict__ st, const TileLane<FR> &at, uint32_t t,
+                                               TileOps<FR> &x)
+{
+    typedef TileLayout<LF, FR> L;
+#pragma unroll
+    for (int f = 0; f < FR; f++) {
+        x.r[f] = tile_read<kOutE2M1, L::rowR>(st + L::offR + at.r[f], t);
+        x.l[f] = tile_read<LF, L::rowL>(st + at.l[f], t);
+    }
+}
+
+template <int FR>
+__device__ __forceinline__ void tile_read_scales(const uint8_t *__restrict__ st, const TileLane<FR> &at,
+                                                 uint32_t (&cl)[FR], uint32_t (&cr)[FR])
+{
+#pragma unroll
+    for (int f = 0; f < FR; f++) {
+        cl[f] = (uint32_t)read_tr8(st + at.sl + 32u * f).x;
+        cr[f] = (uint32_t)read_tr8(st + at.sr + 32u * f).x;
+    }
+}
+
+// The order of what stands before it, to the last scheduling barrier: a few reads behind
+// each product, so that the matrix cores never wait for their issue.
+template <int PRODUCTS, int READS> __device__ __forceinline__ void tile_interleave()
+{
+#pragma unroll
+    for (int k = 0; k < PRODUCTS; k++) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (READS + PRODUCTS - 1) / PRODUCTS, 0);
+    }
+}
+
+// The sums so far are issued before anything below.
+template <int FR> __device__ __forceinline__ void tile_pin(f32x16_t (&acc)[FR][FR])
+{
+#pragma unroll
+    for (int b = 0; b < FR; b++)
+#pragma unroll
+        for (int a = 0; a < FR; a++)
+            if constexpr (FR == 4)      // (in the registers that the sums of a 256-row tile fill)
+                asm volatile("" : "+a"(acc[b][a]));
+            else
+                asm volatile("" : "+v"(acc[b][a]));
+}
+
 template <int LF, int FR, int T>
 __device__ __forceinline__ void tile_products(f32x16_t (&acc)[FR][FR], const TileOps<FR> &x, const uint32_t (&sl)[FR],
                                               const uint32_t (&sr)[FR])
@@ -603,31 +668,22 @@ __global__ __launch_bounds__(kTileThreads, FR == 4 ? 1 : 2) void fp4_tile_kernel
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
 
-    TileOps<FR> x;
-    uint32_t cl[FR], cr[FR];
-#pragma unroll
-    for (int f = 0; f < FR; f++) {
-        x.l[f] = tile_read<LF, L::rowL>(lds + at.l[f], 0);
-        x.r[f] = tile_read<kOutE2M1, L::rowR>(lds + L::offR + at.r[f], 0);
-        cl[f] = (uint32_t)read_tr8(lds + at.sl + 32u * f).x;
-        cr[f] = (uint32_t)read_tr8(lds + at.sr + 32u * f).x;
-    }
+    constexpr int reads = FR * (LF == kOutE2M1 ? 4 : 6);    // instructions of a step's operands
+    TileOps<FR> x, y;
+    uint32_t cl[FR], cr[FR], dl[FR], dr[FR];
+    tile_read_step<LF, FR>(lds, at, 0, x);
+    tile_read_scales<FR>(lds, at, cl, cr);
     uint32_t cur = 0;
     for (uint32_t s = 0; s < n; s++) {
-        // step 0's products; behind them step 1's reads and the copies of a later stage
-        // into the stage before this one, which every wave has read
-        const uint8_t *st = lds + cur * L::stage;
+        // step 1's reads, the copies of a later stage into the stage before this one, which
+        // every wave has read, and step 0's products
         const uint32_t fre = cur == 0 ? L::stages - 1 : cur - 1u;
         const uint32_t nxt = cur == L::stages - 1 ? 0u : cur + 1u;
         __builtin_amdgcn_sched_barrier(0);
-        TileOps<FR> y;
-#pragma unroll
-        for (int f = 0; f < FR; f++) {
-            y.l[f] = tile_read<LF, L::rowL>(st + at.l[f], 1);
-            y.r[f] = tile_read<kOutE2M1, L::rowR>(st + L::offR + at.r[f], 1);
-        }
+        tile_read_step<LF, FR>(lds + cur * L::stage, at, 1, y);
         tile_copy<LF, FR>(sl, sr, lds + fre * L::stage, P, s + L::stages - 1, dense, wave, lane);
         tile_products<LF, FR, 0>(acc, x, cl, cr);
+        tile_pin(acc);
         __builtin_amdgcn_sched_barrier(0);
         // my reads of this stage and my copies of the next one are through; after the
         // barrier everyone's are
@@ -635,22 +691,17 @@ __global__ __launch_bounds__(kTileThreads, FR == 4 ? 1 : 2) void fp4_tile_kernel
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         // step 1's products; behind them the next stage's first reads
-        const uint8_t *sn = lds + nxt * L::stage;
-        uint32_t dl[FR], dr[FR];
-#pragma unroll
-        for (int f = 0; f < FR; f++) {
-            x.l[f] = tile_read<LF, L::rowL>(sn + at.l[f], 0);
-            x.r[f] = tile_read<kOutE2M1, L::rowR>(sn + L::offR + at.r[f], 0);
-            dl[f] = (uint32_t)read_tr8(sn + at.sl + 32u * f).x;
-            dr[f] = (uint32_t)read_tr8(sn + at.sr + 32u * f).x;
-        }
+        tile_read_step<LF, FR>(lds + nxt * L::stage, at, 0, x);
+        tile_read_scales<FR>(lds + nxt * L::stage, at, dl, dr);
         tile_products<LF, FR, 1>(acc, y, cl, cr);
+        tile_interleave<FR * FR, reads + 2 * FR>();
+        tile_pin(acc);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int f = 0; f < FR; f++) {
             cl[f] = dl[f];
             cr[f] = dr[f];
         }
-        __builtin_amdgcn_sched_barrier(0);
         cur = nxt;
     }
     // no copy may land in the LDS that the results take, nor any wave still read there
