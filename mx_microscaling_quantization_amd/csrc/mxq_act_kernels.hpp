@@ -19,8 +19,9 @@
 // (two lane swaps). The rounded values go through the quantize's own helpers
 // (mxq_quantize_kernels.hpp), so the bytes are those of quantizing them by themselves.
 //
-// Memory bounds both passes (bf16, e4m3fn, swiglu of 16384 x 4096: forward 84 us, 5.7 TB/s;
-// backward 111 us, 5.5 TB/s). What costs is the layout of the codes along the rows: 128
+// Memory bounds both passes (bf16, e4m3fn, swiglu of 16384 x 4096, results in memory not
+// written just before: forward 90 us, 5.3 TB/s; backward 114 us, 5.4 TB/s; a copy of 4 GiB
+// runs at 4.7 TB/s). What costs is the layout of the codes along the rows: 128
 // bytes of each view row for a tile. In the backward pass the arithmetic (some 45
 // instructions for each of the tile's values) takes as long as the memory at its peak, under
 // which it hides: with the five instructions that mend four overflow codes left to a
@@ -140,14 +141,28 @@ __device__ __forceinline__ void act_along(const ActBlock &w, int emax, uint64_t 
             u32x4_t x = {code[j][0], code[j][1], code[j][2], code[j][3]};
             u32x4_t y = {code[j][4], code[j][5], code[j][6], code[j][7]};
             uint8_t *p = data + 4u * at;
-            uint32_t next = 16u;
-            if (whole) {     // 64 bytes of lanes 16 apart in each store
-                act_swap(x, y);
-                p = p - 32u * (lane >> 4) + 32u * ((lane >> 4) & 1u) + 16u * (lane >> 5);
-                next = 64u;
+            if (whole) {
+                // An even lane takes the first halves of its own and of the next lane's
+                // (whose view row is two on), that one the second: a store's eight lanes of
+                // four rows apart fill the 128 bytes of a line. Past the caches, as whole
+                // lines go best (forward with the kept values' so too, swiglu, 16384 x
+                // 4096: 110 -> 98 us; with the lines in halves 133 in place of 113, backward).
+                const bool odd = (lane & 1u) != 0;
+                u32x4_t a, b;
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const uint32_t give = odd ? x[k] : y[k];
+                    const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0xB1, 0xF, 0xF, true);
+                    a[k] = odd ? got : x[k];
+                    b[k] = odd ? y[k] : got;
+                }
+                const uint64_t two = 8u * R;    // view rows
+                __builtin_nontemporal_store(a, reinterpret_cast<u32x4_t *>(odd ? p + 16u - two : p));
+                __builtin_nontemporal_store(b, reinterpret_cast<u32x4_t *>(odd ? p + 16u : p + two));
+            } else {
+                *reinterpret_cast<u32x4_t *>(p) = x;
+                *reinterpret_cast<u32x4_t *>(p + 16u) = y;
             }
-            *reinterpret_cast<u32x4_t *>(p) = x;
-            *reinterpret_cast<u32x4_t *>(p + next) = y;
         }
     }
     if ((lane & 3u) == 0)
@@ -223,9 +238,7 @@ __device__ __forceinline__ void act_down(const ActBlock &w, int emax, uint64_t C
             act_swap(x, y);
             // rows of lanes 0 .. 31, then of lanes 32 .. 63 (16 rows of the tensor on)
             uint8_t *p = data + 4u * at + (lane >> 5) * 16u - (lane >> 5) * 16u * C;
-            // past the caches, whole lines as they are (backward, swiglu, 16384 x 4096: 138 -> 111
-            // us; the 64 bytes of a line that act_along writes at a time are not: 113 with
-            // the hint there alone, 133 with it everywhere)
+            // past the caches, whole lines as they are
             __builtin_nontemporal_store(x, reinterpret_cast<u32x4_t *>(p));
             __builtin_nontemporal_store(y, reinterpret_cast<u32x4_t *>(p + 16u * C));
         }
@@ -265,7 +278,8 @@ __device__ __forceinline__ void act_keep(const ActBlock &w, int emax, uint64_t W
             fix_special_codes<IN, OUT, 2>(w[r], e, code[r]);
 #pragma unroll
     for (int r = 0; r < 8; r++)
-        *reinterpret_cast<u32x2_t *>(data + (row0 + r) * W + col) = u32x2_t{code[r][0], code[r][1]};
+        __builtin_nontemporal_store(u32x2_t{code[r][0], code[r][1]},
+                                    reinterpret_cast<u32x2_t *>(data + (row0 + r) * W + col));
     *reinterpret_cast<uint16_t *>(scale + (row0 / 8u) * (W / 4u) + col / 4u) = (uint16_t)(e[0] | e[1] << 8);
 }
 
