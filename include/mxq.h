@@ -5,7 +5,8 @@
  * library allocates nothing, keeps no state between calls and is safe to call
  * from several host threads at once. Every call is asynchronous on the
  * caller's HIP stream: it validates its arguments on the host, enqueues its
- * kernel (the sort of a long list and the clipping: two or more) and returns.
+ * kernel (the sort of a long list, the clipping and the layer for a few
+ * tokens: two or more) and returns.
  * Faults during execution surface at the caller's next synchronisation, not
  * here.
  *

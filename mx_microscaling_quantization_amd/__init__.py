@@ -19,12 +19,13 @@ from typing import NamedTuple
 import torch  # loaded first so that the library binds to torch's HIP runtime
 
 __all__ = [
-    "IN_DTYPES", "OUT_DTYPES", "RES_DTYPES", "ELEM_DTYPES", "ACTIVATIONS", "MXQError", "quantize", "dequantize", "quantize_axis",
-    "scaled_matmul", "scaled_matmul_quantize", "MoEPlan", "moe_rows", "moe_sort", "moe_gather_quantize", "moe_combine",
-    "moe_combine_backward", "grouped_scaled_matmul", "grouped_scaled_matmul_wgrad", "scaled_matmul_fp4",
-    "grouped_scaled_matmul_fp4", "moe_few_tokens", "ActGradients", "act_quantize", "act_quantize_backward",
-    "clip_grad_norm", "grad_norm", "data_bytes", "scale_image_bytes", "result_bytes", "data_shape", "scale_image_shape",
-    "axis_view_shape", "logical_scale_view", "status_string", "library_path", "load",
+    "IN_DTYPES", "OUT_DTYPES", "RES_DTYPES", "ELEM_DTYPES", "ACTIVATIONS", "MXQError", "quantize", "dequantize",
+    "quantize_axis", "scaled_matmul", "scaled_matmul_quantize", "MoEPlan", "moe_rows", "moe_sort",
+    "moe_gather_quantize", "moe_combine", "moe_combine_backward", "grouped_scaled_matmul",
+    "grouped_scaled_matmul_wgrad", "scaled_matmul_fp4", "grouped_scaled_matmul_fp4", "moe_few_tokens", "ActGradients",
+    "act_quantize", "act_quantize_backward", "clip_grad_norm", "grad_norm", "data_bytes", "scale_image_bytes",
+    "result_bytes", "data_shape", "scale_image_shape", "axis_view_shape", "logical_scale_view", "status_string",
+    "library_path", "load",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

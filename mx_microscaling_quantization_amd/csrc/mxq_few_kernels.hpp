@@ -10,8 +10,14 @@
 // of reading the chosen experts' weights once, so nothing else is worth a launch:
 // two kernels, the first up to the activation, the second the down projection and
 // the weighted sum over the slots. There is no sort: each workgroup finds the a-th
-// expert that is in use, and the pairs that chose it, from the ids themselves (up to 1024,
-// in a few hundred cycles, and all workgroups at the same time).
+// expert that is in use, and the pairs that chose it, from the ids themselves (about 2
+// us, all workgroups at the same time).
+//
+// Weights' bytes bound both kernels from some tens of experts on (16 x 4 pairs, 32 experts of
+// e4m3fn, 4096 -> 2 x 2048 -> 4096: 69 and 51 us, 7.0 and 4.7 TB/s); one token's are launches and
+// latency (8 of 128 experts of e2m1, 2048 -> 2 x 768 -> 2048: 9.4 and 9.2 us); with e2m1 and
+// several tokens an expert, widening the weights (61 x 6 pairs of f16, 64 experts, 2016 -> 1440
+// -> 2012: 20 and 20 to 29 us).
 //
 // The activations stay as they come: weights are widened to bf16 in registers, which is
 // exact for every code (3 fraction bits at most) and scale byte but the rarest
