@@ -88,15 +88,24 @@ int run(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs
     //   1024 x 4096 x 14336                  140 (140)  57.3 (41.5)  58.0 (38.8)
     //   2048 x 8192 x 8192                   314 (312)  113 (81.9)   109 (70.7)
     // Groups of up to 64 rows stream their weights whatever their number (64 x 64 rows, 4096 x
-    // 2048: wide 74 (72), 128 x 128 84 (68)). A group's last tile is filled in part, half of
-    // it on average, so 256-row tiles need the rows to make up for it (64 even groups, 4096 x
-    // 2048, 256 x 256 against 128 x 128: 128 rows 137 (94), 101 (81); 256 rows 146 (99), 156
-    // (118); 512 rows 277 (192), 276 (209)), and a short contraction is mostly the stores of
-    // its results, which two tiles on a CU overlap.
+    // 2048: wide 74 (72), 128 x 128 84 (68)).
+    // Between the square tiles the rounds decide: a round of two 128-row tiles on each CU
+    // takes half of one of 256-row tiles' time, 3 % more than that, or 15 % for e2m1 by e2m1
+    // (whose products wait for copies more), but its last round is half as long, and a group's
+    // last tile, filled by half on average, half as large. Uneven groups, 256 x 256 and 128 x
+    // 128: 16 x 2048 rows, 4096 x 4096, 565 (358) and 536 (398); 16 x 512, 171 (112) and 134
+    // (97); 64 x 512, 4096 x 2048, 334 (212) and 309 (223); 8 x 2048, 8192 x 2048, 336 (198) and
+    // 252 (176). A short contraction is mostly the stores of its results, which two tiles on
+    // a CU overlap.
     const int64_t mean = M / groups, kCus = 256;
     const auto tiles = [&](int form) {
         const Form &f = kForms[form];
         return ((M + f.rows - 1) / f.rows) * ((N + f.cols - 1) / f.cols);
+    };
+    const auto rounds = [&](int form, int64_t on_cu) {
+        const Form &f = kForms[form];
+        const int64_t down = offsets ? M / f.rows + (groups + 1) / 2 : (M + f.rows - 1) / f.rows;
+        return (down * ((N + f.cols - 1) / f.cols) + on_cu * kCus - 1) / (on_cu * kCus);
     };
     int form;
     if (tiles(kStreamNarrow) <= kCus)
@@ -105,7 +114,7 @@ int run(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs
         form = kStream;
     else if (mean <= 64)
         form = kStreamWide;
-    else if (tiles(kTile128) <= 2 * kCus || mean <= (lhs_fmt == MXQ_OUT_E2M1 ? 255 : 383) || P <= 256)
+    else if (P <= 256 || rounds(kTile128, 2) * (lhs_fmt == MXQ_OUT_E2M1 ? 115 : 103) < rounds(kTile256, 1) * 200)
         form = kTile128;
     else
         form = kTile256;

@@ -70,6 +70,22 @@ def test_many_rows(M, K, N, fmt, res):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("image", [False, True])
+def test_one_round_of_the_largest_tiles(image, fmt):
+    """As many 256-row tiles as CUs, the last ones in parts, and an odd number of MX blocks."""
+    check(4092, 1056, 4084, fmt, torch.bfloat16 if image else torch.float32, image=image)
+
+
+def test_one_round_of_the_largest_tiles_scale_255_and_nan():
+    def patch(l, ls, r, rs):
+        scale_255(l, ls, r, rs)
+        scale_255_left(l, ls, r, rs)
+        l[3, 4 * 4090 + 1] = 0x7F
+
+    check(4092, 1056, 4084, "e4m3fn", torch.float32, patch, per_block=4)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,K,N", [(3, 160, 36), (90, 96, 132), (600, 288, 1284), (800, 1120, 2820)])
 def test_scale_image(M, K, N, fmt):
     check(M, K, N, fmt, torch.bfloat16, image=True)
@@ -157,6 +173,11 @@ def check_rows(sizes, tail, K, N, fmt, res, first=0, patch=None, per_block=1):
                                                   ([516, 0, 1028], 4, 300, 1088, 1160), ([700, 132, 68, 260], 32, 0, 96, 516)])
 def test_groups(sizes, first, tail, K, N, fmt):
     check_rows(sizes, tail, K, N, fmt, torch.bfloat16, first)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_groups_of_the_largest_tiles(fmt):
+    check_rows([1284, 36, 2200], 60, 1056, 4084, fmt, torch.bfloat16, 4)
 
 
 @pytest.mark.parametrize("sizes,K,N", [([32, 64], 160, 132), ([128, 160, 132], 160, 2600), ([516, 1028], 1088, 1160)])
