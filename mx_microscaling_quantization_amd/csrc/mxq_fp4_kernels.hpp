@@ -205,7 +205,8 @@ template <int FMT> __device__ __forceinline__ i32x8_t fp4_keep_255(const i32x8_t
 // of them, bounded by row_end and N) computed again, 32 x 32 at a time, with every
 // E8M0 byte at its value. The matrix cores read 255 as NaN; here it is fed as 254
 // (2^127) and each flagged block counted twice per flagged side: (A, B) + (A', B) +
-// (A', B') + (A, B') with A' and B' the flagged blocks alone.
+// (A', B') + (A, B') with A' and B' the flagged blocks alone. An infinity of A has its
+// products in (A, B); the other three, which would multiply it by zeros too, leave it out.
 template <int LF, int EPI>
 __device__ __attribute__((noinline)) void fp4_rare_part(const uint8_t *lhs, const uint8_t *lhs_scale,
                                                         const uint8_t *rhs, const uint8_t *rhs_scale, uint32_t P,
@@ -225,8 +226,8 @@ __device__ __attribute__((noinline)) void fp4_rare_part(const uint8_t *lhs, cons
             for (uint32_t s = 0; s < nsteps; s++) {
                 Fp4Raw<LF, 2> r;
                 fp4_load<LF, 2, 0>(r, sa, sb, P, s, nsteps, dense, i, h);
-                const i32x8_t a = fp4_a(r);
-                const i32x8_t ta = fp4_keep_255<LF>(a, r.as == 255u, h);
+                const i32x8_t a = fp4_a(r), fa = mm_finite_codes<F>(a);
+                const i32x8_t ta = fp4_keep_255<LF>(fa, r.as == 255u, h);
                 const uint32_t as = min(r.as, 254u);
 #pragma unroll
                 for (int u = 0; u < 2; u++) {
@@ -235,7 +236,7 @@ __device__ __attribute__((noinline)) void fp4_rare_part(const uint8_t *lhs, cons
                     acc[u] = fp4_mfma<F, 0>(a, b, acc[u], as, bs);
                     acc[u] = fp4_mfma<F, 0>(ta, b, acc[u], as, bs);
                     acc[u] = fp4_mfma<F, 0>(ta, tb, acc[u], as, bs);
-                    acc[u] = fp4_mfma<F, 0>(a, tb, acc[u], as, bs);
+                    acc[u] = fp4_mfma<F, 0>(fa, tb, acc[u], as, bs);
                 }
             }
 #pragma unroll

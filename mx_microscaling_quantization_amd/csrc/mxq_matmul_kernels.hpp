@@ -266,6 +266,26 @@ __device__ __forceinline__ i32x8_t mm_keep_blocks(const i32x8_t &v, bool block0,
     return o;
 }
 
+// The operand's codes with e5m2's infinities and NaN (magnitudes from 0x7C on) zeroed:
+// what a correction may multiply by the zeros of the blocks that it leaves out. In a
+// byte of magnitude bits 0x7C the sum with 4 carries into bit 7, in no other. (e4m3fn has no
+// infinity, and a NaN's results are NaN either way.)
+template <int F> __device__ __forceinline__ i32x8_t mm_finite_codes(const i32x8_t &v)
+{
+    if constexpr (F != MfmaFmt<kOutE5M2>::value) {
+        return v;
+    } else {
+        i32x8_t o;
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const uint32_t bits = (uint32_t)v[k];
+            const uint32_t top = (((bits & 0x7C7C7C7Cu) + 0x04040404u) >> 7) & 0x01010101u;
+            o[k] = (int)(bits & ~(top * 0xFFu));
+        }
+        return o;
+    }
+}
+
 // The K step of one A sub-tile against the wave's 4 B sub-tiles where scale
 // bytes may be 255. An E8M0 byte e stands for 2^(e - 127) for every e, 255
 // (2^128) included -- the consumer's dequant is ldexpf(x, E8M0 - 127) --
