@@ -296,7 +296,8 @@ template <int F> __device__ __forceinline__ i32x8_t mm_finite_codes(const i32x8_
 // With A' and B' the operands keeping only their flagged blocks (dwords
 // 0..3 are block 0, 4..7 block 1), the step adds (A, B) + (A', B) +
 // (A', B') + (A, B'): a block flagged on one side counts twice, on both
-// sides four times, an unflagged one once.
+// sides four times, an unflagged one once. Infinite codes are in (A, B) alone: in
+// the other three they would meet the zeros of the blocks left out, and be NaN.
 template <int F>
 __device__ __forceinline__ void mm_step_255(f32x16_t (&acc)[4], const i32x8_t &aop, const i32x8_t (&bop)[4],
                                             uint32_t as, uint32_t bs, uint32_t h)
@@ -312,15 +313,17 @@ __device__ __forceinline__ void mm_step_255(f32x16_t (&acc)[4], const i32x8_t &a
     const uint32_t other = (uint32_t)__shfl_xor((int)own, 32);
     const uint32_t flags = h ? (own << 1) | other : own | (other << 1);
     const int sa = (int)min(as, 254u);
-    const i32x8_t ta = mm_keep_blocks(aop, (flags >> 8) & 1u, (flags >> 9) & 1u);
+    const i32x8_t fa = mm_finite_codes<F>(aop);
+    const i32x8_t ta = mm_keep_blocks(fa, (flags >> 8) & 1u, (flags >> 9) & 1u);
 #pragma unroll
     for (int u = 0; u < 4; u++) {
         const int sb = (int)(bclamp >> (8 * u));   // byte u in byte 0, op_sel 0
-        const i32x8_t tb = mm_keep_blocks(bop[u], (flags >> (2 * u)) & 1u, (flags >> (2 * u + 1)) & 1u);
+        const i32x8_t fb = mm_finite_codes<F>(bop[u]);
+        const i32x8_t tb = mm_keep_blocks(fb, (flags >> (2 * u)) & 1u, (flags >> (2 * u + 1)) & 1u);
         acc[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(aop, bop[u], acc[u], F, F, 0, sa, 0, sb);
-        acc[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(ta, bop[u], acc[u], F, F, 0, sa, 0, sb);
+        acc[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(ta, fb, acc[u], F, F, 0, sa, 0, sb);
         acc[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(ta, tb, acc[u], F, F, 0, sa, 0, sb);
-        acc[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(aop, tb, acc[u], F, F, 0, sa, 0, sb);
+        acc[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa, tb, acc[u], F, F, 0, sa, 0, sb);
     }
 }
 
