@@ -57,10 +57,13 @@ template <int IN> __device__ __forceinline__ f32x2_t unpack16(uint32_t w)
     }
 }
 
-// 1 / (1 + e^-z): the hardware's 2^x and reciprocal (one step of fp32 each).
+// 1 / (1 + e^-z): the hardware's 2^x and reciprocal (one step of fp32 each). The
+// reciprocal gives zero for results below 2^-126, which gates from -87.4 down to where e^-z leaves
+// fp32 (-88.7) have while silu of them is a normal number, so it is taken of a quarter.
 __device__ __forceinline__ float sigmoid(float z)
 {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
+    const float t = __builtin_amdgcn_exp2f(z * -1.44269504088896340736f);
+    return 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(t, 0.25f, 0.25f));
 }
 
 // A thread's 8 rows x 8 columns as pairs of columns.
