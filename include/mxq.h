@@ -506,8 +506,9 @@ size_t mxq_moe_few_tokens_workspace_bytes(int64_t tokens, int64_t slots, int64_t
  *     e = ids[t][j]
  * in two kernels without a sort, for decode steps. The activations are not
  * quantized: weights are widened exactly, sums are fp32, what is between the
- * products is kept to 16 bits or more of each value, and the sum over the slots is in
- * slot order, rounded once. Scale bytes as for mxq_scaled_matmul, 255 included.
+ * products is kept to 16 bits or more of each value (to 2^-134 below 2^-117), and the sum over
+ * the slots is in slot order, rounded once. Scale bytes as for mxq_scaled_matmul, 0 and 255
+ * included.
  *
  *   x          device pointer, [tokens, K] of in_dtype (enum mxq_in_dtype).
  *   ids        [tokens, slots] expert numbers of id_bytes (4 or 8) bytes; a number

@@ -20,10 +20,11 @@
 // -> 2012: 20 and 30 us).
 //
 // The activations stay as they come: weights are widened to bf16 in registers, which is
-// exact for every code (3 fraction bits at most) and scale byte but the rarest
-// (values below 2^-133 round, and 255 is below), and the products run on the bf16 matrix
+// exact for every code (3 fraction bits at most) and scale byte but the rarest (values below
+// 2^-133, see few_sums_low, and 255, see few_exact), and the products run on the bf16 matrix
 // cores with fp32 sums. An f16 x is the sum of two bf16 numbers exactly; what is
-// between the two products (fp32) is kept as two bf16 numbers, 16 bits of it.
+// between the two products (fp32) is kept as two bf16 numbers, 16 bits of it (fewer below
+// 2^-117, where the second one's last bit is 2^-133).
 //
 // v_mfma_f32_16x16x32_bf16: lane l = i + 16 g supplies values k = 8 g .. 8 g + 7 of row
 // (column) i; result register r of lane l is D[4 g + r][i]. One instruction is one MX
@@ -192,11 +193,37 @@ __device__ __forceinline__ void few_load(FewBlock<FMT> &r, const __amdgpu_buffer
     }
 }
 
-// Column u's 8 values times their scale, as bf16.
-template <int FMT> __device__ __forceinline__ bf16x8_t few_widen(const FewBlock<FMT> &r, int u)
+// The scale byte of column u, in an fp32 number's exponent.
+template <int FMT> __device__ __forceinline__ uint32_t few_exponent(const FewBlock<FMT> &r, int u)
 {
     const uint32_t e = r.scale[u >> 2];
-    const float s = __uint_as_float(((u & 3) < 3 ? e << (23 - 8 * (u & 3)) : e >> 1) & 0x7F800000u);
+    return ((u & 3) < 3 ? e << (23 - 8 * (u & 3)) : e >> 1) & 0x7F800000u;
+}
+
+// Below this byte a code times its scale may be below 2^-133, bf16's last bit (e5m2: below 10,
+// e4m3fn: below 3; e2m1's smallest value times 2^-127 is above it).
+constexpr uint32_t kFewLow = 16;
+
+// Whether this lane has a column with such a byte and a code that is not zero (a quantized block
+// of zeros has byte 1).
+template <int FMT> __device__ __forceinline__ bool few_low(const FewBlock<FMT> &r)
+{
+    if constexpr (FMT == kOutE2M1) {
+        return false;
+    } else {
+        bool low = false;
+        const uint32_t v = r.scale[0] & 0xF0F0F0F0u;    // (a byte of zeros borrows)
+        if (wave_any(((v - 0x01010101u) & ~v & 0x80808080u) != 0))
+#pragma unroll
+            for (int u = 0; u < FewCols<FMT>::lane; u++)
+                low |= few_exponent(r, u) < kFewLow << 23 && ((r.v[0][u] | r.v[1][u]) & 0x7F7F7F7Fu) != 0;
+        return low;
+    }
+}
+
+// Column u's 8 values times s, as bf16.
+template <int FMT> __device__ __forceinline__ bf16x8_t few_widen(const FewBlock<FMT> &r, int u, float s)
+{
     bf16x2_t p[4];
     if constexpr (FMT == kOutE2M1) {
         // byte 1 of a container holds elements 0 and 1, byte 0 elements 2 and 3
@@ -327,9 +354,10 @@ __device__ __attribute__((noinline)) float few_exact(const uint8_t *data, const 
 constexpr int few_depth(int MT) { return MT == 1 ? 4 : MT == 2 ? 3 : 2; }
 
 // MT tiles of 16 pairs from pair `first` on. Wave w takes the MX blocks w, w + waves, .. of the
-// contraction and leaves its sums in registers.
+// contraction and leaves its sums in registers. True where a weight may be too small for
+// that (few_low): then few_sums_low has to take them.
 template <int FMT, int IN, int NM, int MT>
-__device__ __forceinline__ void few_sums(f32x4_t (&acc)[MT][NM][FewCols<FMT>::lane], const __amdgpu_buffer_rsrc_t &data,
+__device__ __forceinline__ bool few_sums(f32x4_t (&acc)[MT][NM][FewCols<FMT>::lane], const __amdgpu_buffer_rsrc_t &data,
                                          const __amdgpu_buffer_rsrc_t &scale, uint32_t C, uint32_t blocks,
                                          const uint32_t (&at_data)[NM], const uint32_t (&at_scale)[NM],
                                          const uint16_t *const (&rows)[MT], uint64_t plane, uint32_t wave, uint32_t waves, uint32_t g)
@@ -340,7 +368,8 @@ __device__ __forceinline__ void few_sums(f32x4_t (&acc)[MT][NM][FewCols<FMT>::la
     FewLeft<IN> x[D][MT];
     const uint32_t n = blocks > wave ? (blocks - wave + waves - 1u) / waves : 0u;
     if (n == 0)
-        return;
+        return false;
+    bool low = false;
     const auto fetch = [&](int q, uint32_t s) {
         const uint32_t b = wave + waves * min(s, n - 1u);   // (past the end: the last one again, not used)
 #pragma unroll
@@ -364,19 +393,73 @@ __device__ __forceinline__ void few_sums(f32x4_t (&acc)[MT][NM][FewCols<FMT>::la
                 for (int t = 0; t < MT; t++)
                     few_terms<IN>(x[q][t], a[t]);
 #pragma unroll
-                for (int k = 0; k < NM; k++)
+                for (int k = 0; k < NM; k++) {
+                    low |= few_low(w[q][k]);
 #pragma unroll
                     for (int u = 0; u < FewCols<FMT>::lane; u++) {
-                        const bf16x8_t b = few_widen<FMT>(w[q][k], u);
+                        const bf16x8_t b = few_widen<FMT>(w[q][k], u, __uint_as_float(few_exponent(w[q][k], u)));
 #pragma unroll
                         for (int t = 0; t < MT; t++)
 #pragma unroll
                             for (int e = terms - 1; e >= 0; e--)
                                 acc[t][k][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][e], b, acc[t][k][u], 0, 0, 0);
                     }
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+    return wave_any(low);
+}
+
+// The same sums where weights are below what bf16 holds: a column's weights under a low byte times
+// 2^64, and its sum over the block (a result register's column is its lane's) times 2^-64.
+template <int FMT, int IN, int NM, int MT>
+__device__ __forceinline__ void few_sums_low(f32x4_t (&acc)[MT][NM][FewCols<FMT>::lane],
+                                             const __amdgpu_buffer_rsrc_t &data, const __amdgpu_buffer_rsrc_t &scale,
+                                             uint32_t C, uint32_t blocks, const uint32_t (&at_data)[NM],
+                                             const uint32_t (&at_scale)[NM], const uint16_t *const (&rows)[MT],
+                                             uint64_t plane, uint32_t wave, uint32_t waves, uint32_t g)
+{
+    constexpr int terms = FewRows<IN>::terms;
+#pragma unroll
+    for (int t = 0; t < MT; t++)
+#pragma unroll
+        for (int k = 0; k < NM; k++)
+#pragma unroll
+            for (int u = 0; u < FewCols<FMT>::lane; u++)
+                acc[t][k][u] = f32x4_t{};
+#pragma unroll 1
+    for (uint32_t s = wave; s < blocks; s += waves) {
+        bf16x8_t a[MT][terms];
+#pragma unroll
+        for (int t = 0; t < MT; t++) {
+            FewLeft<IN> x;
+            few_left<IN>(x, rows[t], plane, 32u * s + 8u * g);
+            few_terms<IN>(x, a[t]);
+        }
+#pragma unroll
+        for (int k = 0; k < NM; k++) {
+            FewBlock<FMT> w;
+            few_load<FMT>(w, data, scale, C, s, at_data[k], at_scale[k]);
+#pragma unroll
+            for (int u = 0; u < FewCols<FMT>::lane; u++) {
+                const uint32_t e = few_exponent(w, u);
+                const bool low = e < kFewLow << 23;
+                const bf16x8_t b = few_widen<FMT>(w, u, __uint_as_float(low ? e + (64u << 23) : e));
+                const float back = low ? 0x1p-64f : 1.0f;
+#pragma unroll
+                for (int t = 0; t < MT; t++) {
+                    f32x4_t sum = {};
+#pragma unroll
+                    for (int q = terms - 1; q >= 0; q--)
+                        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][q], b, sum, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        acc[t][k][u][r] = __builtin_fmaf(sum[r], back, acc[t][k][u][r]);
+                }
+            }
+        }
+    }
 }
 
 // Two values that a workgroup on another XCD will read in the same launch, and such a read.
@@ -422,7 +505,8 @@ __device__ __forceinline__ void few_tiles(float (*sums)[NM * 16][64], uint32_t w
     for (int k = 0; k < NM; k++) {
         const uint32_t col = n0 + U * i, c = col + k * out.cols;
         at_data[k] = col < out.cols ? 2u * g * CB * m.C + CB * c : kDropOffset;
-        at_scale[k] = col < out.cols ? c : kDropOffset;
+        // (where the lane has no column the last ones' scales: a zero would look like a low byte)
+        at_scale[k] = min(col, out.cols - U) + k * out.cols;
     }
     // (a tile's rows past the last pair repeat it; their results are not used)
     const uint16_t *rows[MT];
@@ -439,7 +523,8 @@ __device__ __forceinline__ void few_tiles(float (*sums)[NM * 16][64], uint32_t w
 #pragma unroll
             for (int u = 0; u < U; u++)
                 acc[t][k][u] = f32x4_t{};
-    few_sums<FMT, IN, NM, MT>(acc, data, scale, m.C, K / 32u, at_data, at_scale, rows, plane, wave, waves, g);
+    if (few_sums<FMT, IN, NM, MT>(acc, data, scale, m.C, K / 32u, at_data, at_scale, rows, plane, wave, waves, g))
+        few_sums_low<FMT, IN, NM, MT>(acc, data, scale, m.C, K / 32u, at_data, at_scale, rows, plane, wave, waves, g);
 
     // 16 pairs and four of each lane's columns at a time, through LDS
 #pragma unroll
