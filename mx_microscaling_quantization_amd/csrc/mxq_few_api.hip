@@ -72,11 +72,7 @@ int check_sizes(int64_t tokens, int64_t K, int64_t slots, int64_t experts, int64
 
 int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-int64_t tiles_of(int64_t cols, int fmt)
-{
-    const int64_t tile = fmt == MXQ_OUT_E2M1 ? mxq::FewCols<mxq::kOutE2M1>::all : mxq::FewCols<mxq::kOutE4M3FN>::all;
-    return (cols + tile - 1) / tile;
-}
+int64_t tiles_of(int64_t cols) { return (cols + mxq::kFewCols - 1) / mxq::kFewCols; }
 
 // Waves of a workgroup: eight share a contraction where there are few workgroups, four
 // where there are enough of them to fill the CUs' places.
@@ -91,7 +87,7 @@ size_t mxq_moe_few_tokens_workspace_bytes(int64_t tokens, int64_t slots, int64_t
     if (check_sizes(tokens, 0, slots, 1, F, N) != MXQ_OK)
         return 0;
     const int64_t pairs = tokens * slots;
-    return (size_t)(round16(4 * pairs * F) + round16(4 * pairs * N) + round16(4 * tiles_of(N, MXQ_OUT_E4M3FN) * tokens));
+    return (size_t)(round16(4 * pairs * F) + round16(4 * pairs * N) + round16(4 * tiles_of(N) * tokens));
 }
 
 int mxq_moe_few_tokens(const void *x, int64_t tokens, int64_t K, int in_dtype, const void *ids, int id_bytes,
@@ -122,11 +118,11 @@ int mxq_moe_few_tokens(const void *x, int64_t tokens, int64_t K, int in_dtype, c
     // as many workgroups as any assignment has experts in use; at least one column tile
     // of the first kernel, which also prepares the second one's counters
     const int64_t used = pairs < e ? pairs : e;
-    const int64_t up_tiles = F > 0 ? tiles_of(F, fmt) : 1, down_tiles = tiles_of(N, fmt);
+    const int64_t up_tiles = F > 0 ? tiles_of(F) : 1, down_tiles = tiles_of(N);
     if (!grid_fits(used, up_tiles, mxq::kFewThreads) || !grid_fits(used, down_tiles, mxq::kFewThreads))
         return MXQ_E_OVERFLOW;
     const uint32_t up_waves = waves_of(used * up_tiles), down_waves = waves_of(used * down_tiles);
-    const uint32_t lds = 4u * 16u * 64u;      // a wave's sums of a part with one matrix
+    const uint32_t lds = 4u * 16u * 64u;      // a wave's sums of 16 pairs with one matrix
     uint32_t ut = (uint32_t)up_tiles, dt = (uint32_t)down_tiles;
     uint16_t *h = (uint16_t *)workspace;
     float *y = (float *)((uint8_t *)workspace + round16(4 * (int64_t)pairs * F));

@@ -48,11 +48,8 @@ constexpr uint32_t kFewPairs = 1024;     // pairs a workgroup finds its expert a
 constexpr uint32_t kFewWaves = 8;        // waves that share the contraction, at most
 constexpr uint32_t kFewThreads = 64 * kFewWaves;
 
-// Columns of a lane.
-template <int FMT> struct FewCols {
-    static constexpr int lane = 4;
-    static constexpr uint32_t all = 16u * lane;     // of a workgroup
-};
+constexpr int kFewLaneCols = 4;                     // columns of a lane
+constexpr uint32_t kFewCols = 16u * kFewLaneCols;   // and of a workgroup
 
 // ----------------------------------------------------------------------------
 // Which expert, which pairs
@@ -158,9 +155,9 @@ struct FewMatrix {
 };
 
 template <int FMT> struct FewBlock {
-    static constexpr int dwords = FewCols<FMT>::lane * (FMT == kOutE2M1 ? 2 : 4) / 4;
-    uint32_t v[2][dwords];                       // containers of view rows 2 g and 2 g + 1
-    uint32_t scale[FewCols<FMT>::lane / 4];      // E8M0 of the columns
+    static constexpr int dwords = kFewLaneCols * (FMT == kOutE2M1 ? 2 : 4) / 4;
+    uint32_t v[2][dwords];     // containers of view rows 2 g and 2 g + 1
+    uint32_t scale;            // E8M0 of the columns
 };
 
 // Block b, the lane's columns from its offsets on (past every buffer where it has none).
@@ -184,20 +181,13 @@ __device__ __forceinline__ void few_load(FewBlock<FMT> &r, const __amdgpu_buffer
                 r.v[q][k] = w[k];
         }
     }
-    if constexpr (FewCols<FMT>::lane == 8) {
-        const u32x2_t e = __builtin_amdgcn_raw_buffer_load_b64(scale, at_scale, b * C, 0);
-        r.scale[0] = e.x;
-        r.scale[1] = e.y;
-    } else {
-        r.scale[0] = __builtin_amdgcn_raw_buffer_load_b32(scale, at_scale, b * C, 0);
-    }
+    r.scale = __builtin_amdgcn_raw_buffer_load_b32(scale, at_scale, b * C, 0);
 }
 
 // The scale byte of column u, in an fp32 number's exponent.
 template <int FMT> __device__ __forceinline__ uint32_t few_exponent(const FewBlock<FMT> &r, int u)
 {
-    const uint32_t e = r.scale[u >> 2];
-    return ((u & 3) < 3 ? e << (23 - 8 * (u & 3)) : e >> 1) & 0x7F800000u;
+    return (u < 3 ? r.scale << (23 - 8 * u) : r.scale >> 1) & 0x7F800000u;
 }
 
 // Below this byte a code times its scale may be below 2^-133, bf16's last bit (e5m2: below 10,
@@ -212,10 +202,10 @@ template <int FMT> __device__ __forceinline__ bool few_low(const FewBlock<FMT> &
         return false;
     } else {
         bool low = false;
-        const uint32_t v = r.scale[0] & 0xF0F0F0F0u;    // (a byte of zeros borrows)
+        const uint32_t v = r.scale & 0xF0F0F0F0u;    // (a byte of zeros borrows)
         if (wave_any(((v - 0x01010101u) & ~v & 0x80808080u) != 0))
 #pragma unroll
-            for (int u = 0; u < FewCols<FMT>::lane; u++)
+            for (int u = 0; u < kFewLaneCols; u++)
                 low |= few_exponent(r, u) < kFewLow << 23 && ((r.v[0][u] | r.v[1][u]) & 0x7F7F7F7Fu) != 0;
         return low;
     }
@@ -357,7 +347,7 @@ constexpr int few_depth(int MT) { return MT == 1 ? 4 : MT == 2 ? 3 : 2; }
 // contraction and leaves its sums in registers. True where a weight may be too small for
 // that (few_low): then few_sums_low has to take them.
 template <int FMT, int IN, int NM, int MT>
-__device__ __forceinline__ bool few_sums(f32x4_t (&acc)[MT][NM][FewCols<FMT>::lane], const __amdgpu_buffer_rsrc_t &data,
+__device__ __forceinline__ bool few_sums(f32x4_t (&acc)[MT][NM][kFewLaneCols], const __amdgpu_buffer_rsrc_t &data,
                                          const __amdgpu_buffer_rsrc_t &scale, uint32_t C, uint32_t blocks,
                                          const uint32_t (&at_data)[NM], const uint32_t (&at_scale)[NM],
                                          const uint16_t *const (&rows)[MT], uint64_t plane, uint32_t wave, uint32_t waves, uint32_t g)
@@ -396,7 +386,7 @@ __device__ __forceinline__ bool few_sums(f32x4_t (&acc)[MT][NM][FewCols<FMT>::la
                 for (int k = 0; k < NM; k++) {
                     low |= few_low(w[q][k]);
 #pragma unroll
-                    for (int u = 0; u < FewCols<FMT>::lane; u++) {
+                    for (int u = 0; u < kFewLaneCols; u++) {
                         const bf16x8_t b = few_widen<FMT>(w[q][k], u, __uint_as_float(few_exponent(w[q][k], u)));
 #pragma unroll
                         for (int t = 0; t < MT; t++)
@@ -414,7 +404,7 @@ __device__ __forceinline__ bool few_sums(f32x4_t (&acc)[MT][NM][FewCols<FMT>::la
 // The same sums where weights are below what bf16 holds: a column's weights under a low byte times
 // 2^64, and its sum over the block (a result register's column is its lane's) times 2^-64.
 template <int FMT, int IN, int NM, int MT>
-__device__ __forceinline__ void few_sums_low(f32x4_t (&acc)[MT][NM][FewCols<FMT>::lane],
+__device__ __forceinline__ void few_sums_low(f32x4_t (&acc)[MT][NM][kFewLaneCols],
                                              const __amdgpu_buffer_rsrc_t &data, const __amdgpu_buffer_rsrc_t &scale,
                                              uint32_t C, uint32_t blocks, const uint32_t (&at_data)[NM],
                                              const uint32_t (&at_scale)[NM], const uint16_t *const (&rows)[MT],
@@ -426,7 +416,7 @@ __device__ __forceinline__ void few_sums_low(f32x4_t (&acc)[MT][NM][FewCols<FMT>
 #pragma unroll
         for (int k = 0; k < NM; k++)
 #pragma unroll
-            for (int u = 0; u < FewCols<FMT>::lane; u++)
+            for (int u = 0; u < kFewLaneCols; u++)
                 acc[t][k][u] = f32x4_t{};
 #pragma unroll 1
     for (uint32_t s = wave; s < blocks; s += waves) {
@@ -442,7 +432,7 @@ __device__ __forceinline__ void few_sums_low(f32x4_t (&acc)[MT][NM][FewCols<FMT>
             FewBlock<FMT> w;
             few_load<FMT>(w, data, scale, C, s, at_data[k], at_scale[k]);
 #pragma unroll
-            for (int u = 0; u < FewCols<FMT>::lane; u++) {
+            for (int u = 0; u < kFewLaneCols; u++) {
                 const uint32_t e = few_exponent(w, u);
                 const bool low = e < kFewLow << 23;
                 const bf16x8_t b = few_widen<FMT>(w, u, __uint_as_float(low ? e + (64u << 23) : e));
@@ -495,7 +485,7 @@ __device__ __forceinline__ void few_tiles(float (*sums)[NM * 16][64], uint32_t w
     const uint32_t tid = threadIdx.x, lane = tid & 63u, i = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     constexpr uint32_t CB = FMT == kOutE2M1 ? 2 : 4;
-    constexpr int U = FewCols<FMT>::lane;
+    constexpr int U = kFewLaneCols;
     const __amdgpu_buffer_rsrc_t data =
         __builtin_amdgcn_make_buffer_rsrc((void *)m.data, (short)0, (int)(K / 4u * CB * m.C), kMmBufferFlags);
     const __amdgpu_buffer_rsrc_t scale =
@@ -526,24 +516,23 @@ __device__ __forceinline__ void few_tiles(float (*sums)[NM * 16][64], uint32_t w
     if (few_sums<FMT, IN, NM, MT>(acc, data, scale, m.C, K / 32u, at_data, at_scale, rows, plane, wave, waves, g))
         few_sums_low<FMT, IN, NM, MT>(acc, data, scale, m.C, K / 32u, at_data, at_scale, rows, plane, wave, waves, g);
 
-    // 16 pairs and four of each lane's columns at a time, through LDS
+    // 16 pairs at a time, through LDS
 #pragma unroll
-    for (int part = 0; part < MT * U / 4; part++) {
-        const int t = part / (U / 4), u0 = part % (U / 4) * 4;
+    for (int t = 0; t < MT; t++) {
         if (first + 16u * t >= count)
             break;
-        __syncthreads();     // the last part's sums have been read
+        __syncthreads();     // the last ones' sums have been read
 #pragma unroll
         for (int k = 0; k < NM; k++)
 #pragma unroll
-            for (int u = 0; u < 4; u++)
+            for (int u = 0; u < U; u++)
 #pragma unroll
                 for (int r = 0; r < 4; r++)
-                    sums[wave][(k * 4 + u) * 4 + r][lane] = acc[t][k][u0 + u][r];
+                    sums[wave][(k * U + u) * 4 + r][lane] = acc[t][k][u][r];
         __syncthreads();
         // two columns at a time
         for (uint32_t at = tid; at < 512u; at += 64u * waves) {
-            const uint32_t row = at >> 5, c = 2u * (at & 31u), col = n0 + U * (c >> 2) + u0 + (c & 3u);
+            const uint32_t row = at >> 5, c = 2u * (at & 31u), col = n0 + c;
             if (first + 16u * t + row >= count || col >= out.cols)
                 continue;
             const uint32_t pair = route.pairs[first + 16u * t + row];
@@ -597,11 +586,10 @@ __device__ __forceinline__ void few_expert(float (*sums)[NM * 16][64], uint32_t 
 }
 
 // ----------------------------------------------------------------------------
-// The two kernels: a workgroup (of any number of waves up to 8) has an expert in use and 64 or
-// 128 columns
+// The two kernels: a workgroup (of any number of waves up to 8) has an expert in use and 64 columns
 // ----------------------------------------------------------------------------
 
-extern __shared__ float few_lds[];   // a wave's sums of a part, for each wave
+extern __shared__ float few_lds[];   // a wave's sums of 16 pairs, for each wave
 
 // Waves per SIMD that the registers are to leave room for.
 constexpr int few_room(int fmt, int NM, int MX) { return MX == 4 || NM == 2 ? 2 : fmt == kOutE2M1 ? 3 : 4; }
@@ -625,7 +613,7 @@ __global__ __launch_bounds__(kFewThreads, few_room(FMT, ACT == kActSwiglu ? 2 : 
         const FewMatrix m = {w + (uint64_t)at.expert * (K / 4u) * CB * C,
                              w_scale + (uint64_t)at.expert * (K / 32u) * C, C};
         const FewOut out = {h, nullptr, (uint64_t)pairs * F, F};
-        few_expert<FMT, IN, NM, MT>(sums, blockDim.x / 64u, route, at.count, m, K, x, slots, 0, at.tile * FewCols<FMT>::all,
+        few_expert<FMT, IN, NM, MT>(sums, blockDim.x / 64u, route, at.count, m, K, x, slots, 0, at.tile * kFewCols,
                                     out);
     }
     // for the second kernel: each token's count of pairs that have an expert, up to zero in
@@ -663,7 +651,7 @@ __global__ __launch_bounds__(kFewThreads, few_room(FMT, 1, MX)) void few_down_ke
     FewPlace at;
     if (!few_route<ID>(route, ids, pairs, experts, tiles, at))
         return;
-    const uint32_t n0 = at.tile * FewCols<FMT>::all;
+    const uint32_t n0 = at.tile * kFewCols;
     const FewMatrix m = {w + (uint64_t)at.expert * (F / 4u) * CB * N, w_scale + (uint64_t)at.expert * (F / 32u) * N, N};
     const FewOut o = {nullptr, y, 0, N};
     few_expert<FMT, kInSplit, 1, MX>(sums, blockDim.x / 64u, route, at.count, m, F, h, slots, (uint64_t)pairs * F, n0,
@@ -684,7 +672,7 @@ __global__ __launch_bounds__(kFewThreads, few_room(FMT, 1, MX)) void few_down_ke
     const uint32_t tokens = complete;
     // two columns of two of them at a time, and eight slots' reads of each (one by one, each
     // read waits for the one before)
-    constexpr uint32_t half = FewCols<FMT>::all / 2u;
+    constexpr uint32_t half = kFewCols / 2u;
     const uint32_t items = tokens * half;
     for (uint32_t q0 = threadIdx.x; q0 < items; q0 += 2u * blockDim.x) {
         uint32_t t[2], col[2];
