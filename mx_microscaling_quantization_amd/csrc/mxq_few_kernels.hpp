@@ -633,11 +633,19 @@ __global__ __launch_bounds__(kFewThreads, few_room(FMT, ACT == kActSwiglu ? 2 : 
 
 // A workgroup that has written its columns of its pairs' rows of y says so for each pair's
 // token, and adds up the slots of the tokens that are complete with that, in slot order:
-// the sums do not depend on the order of arrival. Rows are written and read past the L2s
-// (store_shared), so an arrival only has to come after a wave's own stores, which each wave
-// waits for before the barrier in front of it. With ordinary stores and a fence on either
-// side, which writes back and drops whole L2s, this kernel took 440 us instead of 44 (16 x
-// 4 pairs, 32 experts of e4m3fn, 2048 x 4096).
+// the sums do not depend on the order of arrival. No workgroup waits for another.
+//
+// What orders a row of y before its reader, which may be on another XCD: rows are written and
+// read by agent-scope atomics (store_shared), which go past the XCD's L2 to memory that all
+// share, so neither an L2 that still holds a row back nor one that holds an old one is in
+// between. A wave counts a store in vmcnt until memory has acknowledged it; each waits for
+// that count to be zero, then for the barrier, and only then one of them adds to the counter,
+// itself an agent-scope atomic. The reader's loads are issued behind a barrier that follows
+// the counter's answer. That is the target's rule for such accesses, and not HIP's memory
+// model, which would have a release before the counter and an acquire behind it: these also write
+// back, and drop, everything else in an L2, each time (16 x 4 pairs, 32 experts of e4m3fn, 4096 ->
+// 2048 -> 4096, the whole layer: 115 us; with the release 333, with both 340; with ordinary
+// stores and fences this kernel alone 440).
 template <int FMT, int IN, int MX, typename ID>
 __global__ __launch_bounds__(kFewThreads, few_room(FMT, 1, MX)) void few_down_kernel(
     const uint16_t *__restrict__ h, uint32_t F, const void *__restrict__ ids, uint32_t pairs, uint32_t slots,
