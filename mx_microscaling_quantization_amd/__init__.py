@@ -775,8 +775,9 @@ def scaled_matmul_fp4(lhs: torch.Tensor, lhs_scale: torch.Tensor, rhs: torch.Ten
 
     ``lhs`` is [P, 4M] (e2m1: [P, 2M]) and ``rhs`` [P, 2N] with K = 4P; their scales are
     images [P, M] and [P, N], or dense [P/8, M] and [P/8, N] with ``dense_scale``. M is
-    any number of rows, N a multiple of 4. Returns [M, N] float32 or bfloat16;
-    arithmetic as in :func:`scaled_matmul`.
+    any number of rows (from some hundred on, multiples of 4 are up to 4.6 times as fast),
+    N a multiple of 4. Returns [M, N] float32 or bfloat16; arithmetic as in
+    :func:`scaled_matmul`.
     """
     lib = load()
     code, M = _fp4_result(lhs, lhs_fmt, res_dtype)

@@ -14,8 +14,8 @@
 // us, all workgroups at the same time).
 //
 // Weights' bytes bound both kernels from some tens of experts on (16 x 4 pairs, 32 experts of
-// e4m3fn, 4096 -> 2 x 2048 -> 4096: 69 and 51 us, 7.0 and 4.7 TB/s); one token's are launches and
-// latency (8 of 128 experts of e2m1, 2048 -> 2 x 768 -> 2048: 9.4 and 9.2 us); with e2m1 and
+// e4m3fn, 4096 -> 2 x 2048 -> 4096: 69 and 48 us, 7.0 and 5.0 TB/s); one token's are launches and
+// latency (8 of 128 experts of e2m1, 2048 -> 2 x 768 -> 2048: 9 to 10 and 9 us); with e2m1 and
 // several tokens an expert, widening the weights (61 x 6 pairs of f16, 64 experts, 2016 -> 1440
 // -> 2012: 20 and 30 us).
 //

@@ -118,7 +118,8 @@ int run(const void *lhs, const void *lhs_scale, const void *rhs, const void *rhs
         form = kTile128;
     else
         form = kTile256;
-    // the square tiles copy 16 bytes of containers and 4 scale bytes at a time
+    // the square tiles copy 16 bytes of containers and 4 scale bytes at a time, which a pitch of other
+    // row counts does not allow (2047 and 2048 x 8192 x 8192: 319 (317) and 109 (70) us)
     if (M % 4 != 0 && form <= kTile128)
         form = kStreamWide;
 
